@@ -11,6 +11,7 @@
 #include <cuda_runtime.h>
 
 #include "la_internal.h"
+#include "la_serving.h"
 #include "la_state.h"
 #include "la_device.cuh"
 
@@ -624,6 +625,299 @@ la_status la_state_pool_encode(const la_pool* pool, int32_t n, const int32_t* sl
 la_status la_state_pool_decode(const la_pool* pool, int32_t n, const int32_t* slots, float* dense, int32_t* err_word,
                                void* stream) {
   return q8_codec(pool, n, slots, dense, 0, err_word, stream);
+}
+
+// ---- drafted token trees ------------------------------------------------------------------
+
+static la_status check_nodes(int32_t n_seqs, int32_t total_nodes, int32_t max_nodes, int32_t n_v_heads) {
+  if (n_seqs < 0 || total_nodes < 0 || max_nodes < 1) return LA_ERR_SHAPE;
+  if (max_nodes > LA_TREE_MAX_NODES) return LA_ERR_UNSUPPORTED;
+  if ((int64_t)n_seqs * n_v_heads > INT32_MAX) return LA_ERR_SHAPE;
+  return LA_OK;
+}
+
+la_status la_state_tree(la_rule rule, const la_pool* src, const int32_t* read_slot, int32_t n_seqs,
+                        const int32_t* cu_nodes, int32_t total_nodes, const int32_t* parent, int32_t max_nodes,
+                        const void* q, const void* k, const void* v, la_dtype io, const float* g, const float* beta,
+                        float scale, void* o, float* u, int32_t* err_word, void* stream) {
+  if (rule < LA_RULE_LINEAR || rule > LA_RULE_KDA) return LA_ERR_UNSUPPORTED;
+  if (!err_word) return LA_ERR_NULL;
+  la_status st = check_pool(src);
+  if (st != LA_OK) return st;
+  const la_shape& s = src->shape;
+  if ((st = check_nodes(n_seqs, total_nodes, max_nodes, s.n_v_heads)) != LA_OK) return st;
+  if (!elem_bytes(io) || !la_shape_supported(s.d_k, s.d_v)) return LA_ERR_UNSUPPORTED;
+  if (n_seqs == 0) return LA_OK;
+  if (!cu_nodes) return LA_ERR_NULL;
+  if (total_nodes > 0) {
+    if (!parent || !q || !k || !v || !o) return LA_ERR_NULL;
+    if (uses_gate(rule) && !g) return LA_ERR_NULL;
+    if (uses_beta(rule) && !beta) return LA_ERR_NULL;
+  }
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(u, 16) ||
+      !aligned(g, gate_align(rule)) || !aligned(beta, 4) || !aligned(read_slot, 4) || !aligned(cu_nodes, 4) ||
+      !aligned(parent, 4) || !aligned(err_word, 4))
+    return LA_ERR_ALIGN;
+  if (!read_slot && n_seqs > src->n_slots) return LA_ERR_SHAPE;
+  la::TreeLaunchFn fn = la::find_tree(rule, s.d_k, s.d_v, src->dtype, io);
+  if (!fn) return LA_ERR_UNSUPPORTED;
+  la::TreeParams p{};
+  p.src = src->data;
+  p.src_slots = src->n_slots;
+  p.src_n_hp = src->dtype == LA_Q8 ? src->n_hp : 0;
+  p.src_mask = src->dtype == LA_Q8 ? src->hp_mask : nullptr;
+  p.read_slot = read_slot;
+  p.n_seqs = n_seqs;
+  p.cu = cu_nodes;
+  p.total = total_nodes;
+  p.parent = parent;
+  p.max_nodes = max_nodes;
+  p.n_qk_heads = s.n_qk_heads;
+  p.n_v_heads = s.n_v_heads;
+  p.use_beta = p.predicts = uses_beta(rule);
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.g = uses_gate(rule) ? g : nullptr;
+  p.beta = uses_beta(rule) ? beta : nullptr;
+  p.scale = scale;
+  p.o = o;
+  p.u = u;
+  p.err = err_word;
+  return cuda_status(fn(p, static_cast<cudaStream_t>(stream)));
+}
+
+la_status la_tree_accept(int32_t n_seqs, const int32_t* cu_nodes, int32_t total_nodes, const int32_t* parent,
+                         int32_t max_nodes, const int32_t* draft, const int32_t* target, const int32_t* root,
+                         int32_t* leaf, int32_t* count, int32_t* next, int32_t* err_word, void* stream) {
+  if (!err_word) return LA_ERR_NULL;
+  const la_status st = check_nodes(n_seqs, total_nodes, max_nodes, 1);
+  if (st != LA_OK) return st;
+  if (n_seqs == 0) return LA_OK;
+  if (!cu_nodes || !root || !leaf || !count || !next) return LA_ERR_NULL;
+  if (total_nodes > 0 && (!parent || !draft || !target)) return LA_ERR_NULL;
+  if (!aligned(cu_nodes, 4) || !aligned(parent, 4) || !aligned(draft, 4) || !aligned(target, 4) || !aligned(root, 4) ||
+      !aligned(leaf, 4) || !aligned(count, 4) || !aligned(next, 4) || !aligned(err_word, 4))
+    return LA_ERR_ALIGN;
+  la::TreeAcceptParams p{n_seqs, cu_nodes, total_nodes, parent, max_nodes, draft, target, root, leaf, count, next, err_word};
+  return cuda_status(la::launch_tree_accept(p, static_cast<cudaStream_t>(stream)));
+}
+
+la_status la_state_tree_commit(la_rule rule, const la_pool* src, const int32_t* read_slot, const la_pool* dst,
+                               const int32_t* write_slot, int32_t n_seqs, const int32_t* cu_nodes, int32_t total_nodes,
+                               const int32_t* parent, const int32_t* leaf, int32_t max_nodes, const void* k,
+                               la_dtype io, const float* g, const float* u, int32_t* err_word, void* stream) {
+  if (rule < LA_RULE_LINEAR || rule > LA_RULE_KDA) return LA_ERR_UNSUPPORTED;
+  if (!err_word) return LA_ERR_NULL;
+  la_status st = check_pool(src);
+  if (st != LA_OK) return st;
+  if ((st = check_pool(dst)) != LA_OK) return st;
+  const la_shape& s = src->shape;
+  if (!same_shape(s, dst->shape)) return LA_ERR_SHAPE;
+  if ((st = check_nodes(n_seqs, total_nodes, max_nodes, s.n_v_heads)) != LA_OK) return st;
+  if (src->dtype != dst->dtype || !elem_bytes(io) || !la_shape_supported(s.d_k, s.d_v)) return LA_ERR_UNSUPPORTED;
+  const bool q8 = src->dtype == LA_Q8;
+  if (q8 && src->n_hp != dst->n_hp) return LA_ERR_SHAPE;
+  if (q8 && src->data == dst->data && src->hp_mask != dst->hp_mask) return LA_ERR_ALIAS;
+  if (n_seqs == 0) return LA_OK;
+  if (!cu_nodes || !leaf) return LA_ERR_NULL;
+  if (total_nodes > 0 && (!parent || !k || !u || (uses_gate(rule) && !g))) return LA_ERR_NULL;
+  if (!aligned(k, 16) || !aligned(u, 16) || !aligned(g, gate_align(rule)) || !aligned(read_slot, 4) ||
+      !aligned(write_slot, 4) || !aligned(cu_nodes, 4) || !aligned(parent, 4) || !aligned(leaf, 4) ||
+      !aligned(err_word, 4))
+    return LA_ERR_ALIGN;
+  if ((!read_slot && n_seqs > src->n_slots) || (!write_slot && n_seqs > dst->n_slots)) return LA_ERR_SHAPE;
+  la::TreeCommitLaunchFn fn = la::find_tree_commit(rule, s.d_k, s.d_v, src->dtype, io);
+  if (!fn) return LA_ERR_UNSUPPORTED;
+  la::TreeCommitParams p{};
+  p.src = src->data;
+  p.src_slots = src->n_slots;
+  p.read_slot = read_slot;
+  p.dst = dst->data;
+  p.dst_slots = dst->n_slots;
+  p.write_slot = write_slot;
+  p.n_hp = q8 ? src->n_hp : 0;
+  p.src_mask = q8 ? src->hp_mask : nullptr;
+  p.dst_mask = q8 ? dst->hp_mask : nullptr;
+  p.n_seqs = n_seqs;
+  p.cu = cu_nodes;
+  p.total = total_nodes;
+  p.parent = parent;
+  p.leaf = leaf;
+  p.max_nodes = max_nodes;
+  p.n_qk_heads = s.n_qk_heads;
+  p.n_v_heads = s.n_v_heads;
+  p.k = k;
+  p.g = uses_gate(rule) ? g : nullptr;
+  p.u = u;
+  p.err = err_word;
+  return cuda_status(fn(p, static_cast<cudaStream_t>(stream)));
+}
+
+// ---- beam search ----------------------------------------------------------------------------
+
+static la_status check_beam(int32_t n_seqs, int32_t n_beams, int32_t vocab, int32_t n_out) {
+  if (n_seqs < 0 || n_beams < 1 || vocab < 1 || n_out < 1) return LA_ERR_SHAPE;
+  if (n_beams > LA_BEAM_MAX || n_out > LA_BEAM_MAX) return LA_ERR_UNSUPPORTED;
+  if ((int64_t)n_out > (int64_t)n_beams * vocab || (int64_t)n_seqs * n_beams > INT32_MAX / 64) return LA_ERR_SHAPE;
+  return LA_OK;
+}
+
+size_t la_beam_workspace_bytes(int32_t n_seqs, int32_t n_beams, int32_t vocab, int32_t n_out) {
+  if (check_beam(n_seqs, n_beams, vocab, n_out) != LA_OK) return 0;
+  return la::beam_workspace_bytes(n_seqs, n_beams, vocab, n_out);
+}
+
+la_status la_beam_select(int32_t n_seqs, int32_t n_beams, int32_t vocab, const void* logits, la_dtype io,
+                         int64_t row_stride, const float* cum_score, const int32_t* finished, int32_t eos_token,
+                         int32_t n_out, int32_t* parent, int32_t* token, float* score, int32_t* finished_out,
+                         void* workspace, size_t workspace_bytes, void* stream) {
+  const la_status st = check_beam(n_seqs, n_beams, vocab, n_out);
+  if (st != LA_OK) return st;
+  if (!elem_bytes(io)) return LA_ERR_UNSUPPORTED;
+  if (row_stride < vocab || (finished && (eos_token < 0 || eos_token >= vocab))) return LA_ERR_SHAPE;
+  if (n_seqs == 0) return LA_OK;
+  if (!logits || !cum_score || !parent || !token || !score || !workspace) return LA_ERR_NULL;
+  if (!aligned(logits, elem_bytes(io)) || !aligned(cum_score, 4) || !aligned(finished, 4) || !aligned(parent, 4) ||
+      !aligned(token, 4) || !aligned(score, 4) || !aligned(finished_out, 4) || !aligned(workspace, 16))
+    return LA_ERR_ALIGN;
+  if (workspace_bytes < la::beam_workspace_bytes(n_seqs, n_beams, vocab, n_out)) return LA_ERR_SHAPE;
+  la::BeamParams p{};
+  p.n_seqs = n_seqs;
+  p.n_beams = n_beams;
+  p.vocab = vocab;
+  p.n_out = n_out;
+  p.logits = logits;
+  p.io = io;
+  p.row_stride = row_stride;
+  p.cum = cum_score;
+  p.finished = finished;
+  p.eos = eos_token;
+  p.parent = parent;
+  p.token = token;
+  p.score = score;
+  p.finished_out = finished_out;
+  p.workspace = workspace;
+  return cuda_status(la::launch_beam_select(p, static_cast<cudaStream_t>(stream)));
+}
+
+// ---- slots over all layers --------------------------------------------------------------------
+
+la_status la_pool_slab(const la_pool* pool, la_slab* slab) {
+  if (!slab) return LA_ERR_NULL;
+  const la_status st = check_pool(pool);
+  if (st != LA_OK) return st;
+  slab->data = pool->data;
+  slab->slot_bytes = slot_bytes(pool);
+  slab->n_slots = pool->n_slots;
+  return LA_OK;
+}
+
+static la_status slab_list(const la_slab* slabs, int32_t n_slabs, la::SlabList* out) {
+  if (!slabs) return LA_ERR_NULL;
+  if (n_slabs < 1) return LA_ERR_SHAPE;
+  if (n_slabs > la::kMaxSlabs) return LA_ERR_UNSUPPORTED;
+  out->n = n_slabs;
+  for (int32_t l = 0; l < n_slabs; ++l) {
+    if (!slabs[l].data) return LA_ERR_NULL;
+    if (slabs[l].n_slots < 0 || slabs[l].n_slots != slabs[0].n_slots || slabs[l].slot_bytes <= 0 ||
+        slabs[l].slot_bytes % 16)
+      return LA_ERR_SHAPE;
+    if (!aligned(slabs[l].data, 16)) return LA_ERR_ALIGN;
+    out->data[l] = slabs[l].data;
+    out->bytes[l] = slabs[l].slot_bytes;
+  }
+  return LA_OK;
+}
+
+la_status la_state_pool_reorder(const la_slab* slabs, int32_t n_slabs, int32_t n_seqs, int32_t n_beams,
+                                const int32_t* slots, const int32_t* parent, int32_t* new_slots, int32_t* err_word,
+                                void* stream) {
+  if (!err_word) return LA_ERR_NULL;
+  la::SlabList list;
+  const la_status st = slab_list(slabs, n_slabs, &list);
+  if (st != LA_OK) return st;
+  if (n_seqs < 0 || n_beams < 1 || (int64_t)n_seqs * n_beams > INT32_MAX) return LA_ERR_SHAPE;
+  if (n_beams > LA_BEAM_MAX) return LA_ERR_UNSUPPORTED;
+  if (n_seqs == 0) return LA_OK;
+  if (!slots || !parent || !new_slots) return LA_ERR_NULL;
+  if (!aligned(slots, 4) || !aligned(parent, 4) || !aligned(new_slots, 4) || !aligned(err_word, 4)) return LA_ERR_ALIGN;
+  if (new_slots == slots || new_slots == parent) return LA_ERR_ALIAS;
+  return cuda_status(la::launch_pool_reorder(list, slabs[0].n_slots, n_seqs, n_beams, slots, parent, new_slots, err_word,
+                                             static_cast<cudaStream_t>(stream)));
+}
+
+static la_status check_ref(const int32_t* ref, int32_t n_slots, int32_t n, const int32_t* slots, const int32_t* err_word) {
+  if (!err_word) return LA_ERR_NULL;
+  if (n_slots < 0 || n < 0) return LA_ERR_SHAPE;
+  if (n > 0 && (!slots || (n_slots > 0 && !ref))) return LA_ERR_NULL;
+  if (!aligned(ref, 4) || !aligned(slots, 4) || !aligned(err_word, 4)) return LA_ERR_ALIGN;
+  return n > 0 && slots == ref ? LA_ERR_ALIAS : LA_OK;
+}
+
+la_status la_state_pool_alloc(int32_t* ref, int32_t n_slots, int32_t n, int32_t* slots, int32_t* err_word, void* stream) {
+  const la_status st = check_ref(ref, n_slots, n, slots, err_word);
+  if (st != LA_OK || n == 0) return st;
+  return cuda_status(la::launch_pool_alloc(ref, n_slots, n, slots, err_word, static_cast<cudaStream_t>(stream)));
+}
+
+la_status la_state_pool_share(int32_t* ref, int32_t n_slots, int32_t n, const int32_t* slots, int32_t* err_word,
+                              void* stream) {
+  const la_status st = check_ref(ref, n_slots, n, slots, err_word);
+  if (st != LA_OK || n == 0) return st;
+  return cuda_status(la::launch_pool_ref(ref, n_slots, n, slots, 1, err_word, static_cast<cudaStream_t>(stream)));
+}
+
+la_status la_state_pool_free(int32_t* ref, int32_t n_slots, int32_t n, const int32_t* slots, int32_t* err_word,
+                             void* stream) {
+  const la_status st = check_ref(ref, n_slots, n, slots, err_word);
+  if (st != LA_OK || n == 0) return st;
+  return cuda_status(la::launch_pool_ref(ref, n_slots, n, slots, -1, err_word, static_cast<cudaStream_t>(stream)));
+}
+
+la_status la_state_pool_fork(const la_slab* slabs, int32_t n_slabs, int32_t* ref, int32_t n, const int32_t* src_slots,
+                             int32_t* new_slots, int32_t* err_word, void* stream) {
+  if (!err_word) return LA_ERR_NULL;
+  la::SlabList list;
+  la_status st = slab_list(slabs, n_slabs, &list);
+  if (st != LA_OK) return st;
+  if ((st = check_ref(ref, slabs[0].n_slots, n, new_slots, err_word)) != LA_OK || n == 0) return st;
+  if (!src_slots) return LA_ERR_NULL;
+  if (!aligned(src_slots, 4)) return LA_ERR_ALIGN;
+  if (src_slots == new_slots || src_slots == ref) return LA_ERR_ALIAS;
+  return cuda_status(la::launch_pool_fork(list, ref, slabs[0].n_slots, n, src_slots, new_slots, err_word,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+la_status la_state_pool_compact(const la_slab* slabs, int32_t n_slabs, const int32_t* ref, int32_t* new_ref,
+                                int32_t* remap, int32_t* moves, int32_t* counts, int32_t* err_word, void* stream) {
+  if (!err_word) return LA_ERR_NULL;
+  la::SlabList list;
+  const la_status st = slab_list(slabs, n_slabs, &list);
+  if (st != LA_OK) return st;
+  if (!counts) return LA_ERR_NULL;
+  if (slabs[0].n_slots > 0 && (!ref || !new_ref || !remap || !moves)) return LA_ERR_NULL;
+  if (!aligned(ref, 4) || !aligned(new_ref, 4) || !aligned(remap, 4) || !aligned(moves, 4) || !aligned(counts, 4) ||
+      !aligned(err_word, 4))
+    return LA_ERR_ALIGN;
+  const int32_t* all[5] = {ref, new_ref, remap, moves, counts};
+  for (int i = 0; i < 5; ++i)
+    for (int j = 0; j < i; ++j)
+      if (all[i] && all[i] == all[j]) return LA_ERR_ALIAS;
+  return cuda_status(la::launch_pool_compact(list, slabs[0].n_slots, ref, new_ref, remap, moves, counts, err_word,
+                                             static_cast<cudaStream_t>(stream)));
+}
+
+la_status la_state_pool_remap(int64_t n, const int32_t* table, int32_t n_slots, const int32_t* remap, int32_t* new_table,
+                              int32_t* err_word, void* stream) {
+  if (!err_word) return LA_ERR_NULL;
+  if (n < 0 || n > INT32_MAX || n_slots < 0) return LA_ERR_SHAPE;
+  if (n == 0) return LA_OK;
+  if (!table || !new_table || (n_slots > 0 && !remap)) return LA_ERR_NULL;
+  if (!aligned(table, 4) || !aligned(remap, 4) || !aligned(new_table, 4) || !aligned(err_word, 4)) return LA_ERR_ALIGN;
+  if (new_table == remap) return LA_ERR_ALIAS;
+  return cuda_status(la::launch_pool_remap(n, table, n_slots, remap, new_table, err_word,
+                                           static_cast<cudaStream_t>(stream)));
 }
 
 size_t la_pool_slot_bytes(const la_pool* pool) {

@@ -1,0 +1,384 @@
+// la_tree.cuh -- drafted token trees over the slot pool (la_state_tree, la_state_tree_commit).
+//
+// A request's drafted tokens form a tree below its current state S0.  Node t with parent p
+// continues S_p:  S_t = a_t S_p + k_t u_t^T,  u_t = b_t (v_t - c_t S_p^T k_t),  o_t = scale
+// S_t^T q_t.  No S_t is ever formed.  With D_ts the product of the gates on the path from s
+// (exclusive) down to t and Gamma_t that from the root (kda: one product per key channel),
+// unrolling the recurrence along the path gives
+//   u_t = b_t (v_t - [S0^T (Gamma_t k_t) + sum_{s above t} (k_t . D_ts k_s) u_s])    (delta rules)
+//   o_t = scale (S0^T (Gamma_t q_t) + sum_{s above or at t} (q_t . D_ts k_s) u_s)
+// so S0 is read once and nothing is written but the outputs (and u, for the commit).  The
+// products D_ts are taken step by step along the path, never as ratios, so a gate of zero or
+// of either sign is exact, and sums run over a node's own path only, so a non-finite value in
+// one branch does not reach another.
+#pragma once
+
+#include "la_device.cuh"
+#include "la_serving.h"
+
+namespace la {
+namespace tree {
+
+constexpr int kMaxNodes = LA_TREE_MAX_NODES;
+
+// One (pool dtype) element reader of a state tile by (row, column).
+template <typename ST>
+struct TileReader {
+  const ST* tile;
+  __device__ __forceinline__ void init(const void* pool, int64_t tile_index, int dk, int dv, int, const int*) {
+    tile = static_cast<const ST*>(pool) + tile_index * dk * dv;
+  }
+  template <int DV>
+  __device__ __forceinline__ float at(int i, int j) const { return io_load(tile + i * DV + j); }
+};
+// q8: row_info[i] = rank of row i in its block, times two, plus one for a BF16 row
+template <>
+struct TileReader<q8_t> {
+  const unsigned char* tile;
+  int n8;
+  const int* row_info;
+  __device__ __forceinline__ void init(const void* pool, int64_t tile_index, int dk, int dv, int n_hp, const int* info) {
+    tile = static_cast<const unsigned char*>(pool) + tile_index * q8_tile_bytes(dk, dv, n_hp);
+    n8 = dk - n_hp;
+    row_info = info;
+  }
+  template <int DV>
+  __device__ __forceinline__ float at(int i, int j) const {
+    constexpr int NG = DV / 32;
+    const int e = row_info[i], idx = e >> 1;
+    if (e & 1)
+      return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(tile + n8 * DV + n8 * NG * 4)[idx * DV + j]);
+    return __fmul_rn((float)reinterpret_cast<const int8_t*>(tile)[idx * DV + j],
+                     reinterpret_cast<const float*>(tile + n8 * DV)[idx * NG + (j >> 5)]);
+  }
+};
+
+// Ranks of a q8 head's rows (threads of the CTA, dk <= blockDim.x); false for a mask that does not hold n_hp rows.
+__device__ __forceinline__ bool q8_rows(const uint32_t* mask, int dk, int n_hp, int* row_info) {
+  int count = 0;
+  for (int w = 0; w < dk / 32; ++w) count += __popc(__ldg(mask + w));
+  if (count != n_hp) return false;
+  for (int i = threadIdx.x; i < dk; i += blockDim.x) {
+    int below = 0;
+    for (int w = 0; w < i / 32; ++w) below += __popc(__ldg(mask + w));
+    const uint32_t m = __ldg(mask + i / 32);
+    below += __popc(m & ((1u << (i & 31)) - 1u));
+    const bool hp = (m >> (i & 31)) & 1u;
+    row_info[i] = hp ? 2 * below + 1 : 2 * (i - below);
+  }
+  return true;
+}
+
+// The nodes of sequence b: c0 and their number, -1 when the offsets or the count are wrong.
+__device__ __forceinline__ int tree_span(const int32_t* cu, int total, int max_nodes, int b, int& c0) {
+  c0 = __ldg(cu + b);
+  const int c1 = __ldg(cu + b + 1);
+  if (c0 < 0 || c1 < c0 || c1 > total) return -1;
+  return c1 - c0 > max_nodes ? -2 : c1 - c0;
+}
+__device__ __forceinline__ uint32_t span_error(int n) { return n == -1 ? LA_DEVERR_CU_SEQLENS : LA_DEVERR_TREE; }
+
+// ---- verification ------------------------------------------------------------------------
+
+constexpr int kTreeThreads = 128;
+constexpr int kBlock = 16;  // nodes whose products with S0 are formed in one pass over it
+
+template <int DK, int DV>
+__host__ __device__ constexpr int tree_smem(int rows, bool kda) {
+  return 4 * (rows * DK * (kda ? 3 : 2) + 2 * rows * rows + rows * DV + 2 * kBlock * DV + 3 * rows + DK);
+}
+
+// One CTA per (sequence, state head), FP32 throughout.  The pair coefficients are one warp
+// per node walking to the root; the products with S0 one column of d_v per thread (kBlock
+// nodes per pass); the substitution one column per thread, node after node.
+template <typename ST, typename IT, int DK, int DV, bool KDA>
+__global__ void __launch_bounds__(kTreeThreads) tree_kernel(const TreeParams p, int rows) {
+  extern __shared__ __align__(16) float sm[];
+  float* K = sm;                        // [rows][DK]
+  float* Q = K + rows * DK;             // [rows][DK] (kda: scaled by Gamma after the pair pass)
+  float* KG = Q + rows * DK;            // [rows][DK] kda: K scaled by Gamma
+  float* KK = KDA ? KG + rows * DK : KG;  // [rows][rows]
+  float* QK = KK + rows * rows;
+  float* U = QK + rows * rows;          // [rows][DV]
+  float* buf = U + rows * DV;           // [kBlock][2][DV]
+  float* gamma = buf + 2 * kBlock * DV; // [rows]
+  float* gate = gamma + rows;           // [rows] (scalar gates)
+  int* par = reinterpret_cast<int*>(gate + rows);  // [rows]
+  int* row_info = par + rows;           // [DK] (q8)
+
+  const int H = p.n_v_heads;
+  const int b = blockIdx.x / H, h = blockIdx.x % H;
+  const int hq = h / (H / p.n_qk_heads);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int c0;
+  const int n = tree_span(p.cu, p.total, p.max_nodes, b, c0);
+  if (n < 0) {
+    if (tid == 0) report(p.err, span_error(n));
+    return;
+  }
+  if (n == 0) return;
+  const int slot = p.read_slot ? __ldg(p.read_slot + b) : b;
+  if (slot < 0 || slot >= p.src_slots) {
+    if (tid == 0) report(p.err, LA_DEVERR_READ_SLOT);
+    return;
+  }
+  bool bad = false;
+  for (int t = tid; t < n; t += kTreeThreads) {
+    const int pt = __ldg(p.parent + c0 + t);
+    bad |= pt < -1 || pt >= t;
+    par[t] = pt;
+    if (!KDA) gate[t] = p.g ? __ldg(p.g + (int64_t)(c0 + t) * H + h) : 1.0f;
+  }
+  if (__syncthreads_or(bad)) {
+    if (tid == 0) report(p.err, LA_DEVERR_TREE);
+    return;
+  }
+  bool mask_ok = true;
+  if constexpr (sizeof(ST) == sizeof(q8_t)) mask_ok = q8_rows(p.src_mask + h * (DK / 32), DK, p.src_n_hp, row_info);
+  if (!mask_ok) {
+    if (tid == 0) report(p.err, LA_DEVERR_Q8_MASK);
+    return;
+  }
+  const IT* gq = static_cast<const IT*>(p.q);
+  const IT* gk = static_cast<const IT*>(p.k);
+  const IT* gv = static_cast<const IT*>(p.v);
+  for (int e = tid; e < n * DK; e += kTreeThreads) {
+    const int64_t at = ((int64_t)(c0 + e / DK) * p.n_qk_heads + hq) * DK + e % DK;
+    K[e] = io_load(gk + at);
+    Q[e] = io_load(gq + at);
+  }
+  __syncthreads();
+
+  // pair coefficients and Gamma: one warp per node, lane = DK / 32 key channels
+  constexpr int CH = DK / 32 > 0 ? DK / 32 : 1;
+  const bool on = lane * CH < DK;
+  for (int t = warp; t < n; t += kTreeThreads / 32) {
+    float kt[CH], qt[CH], d[CH];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      kt[c] = on ? K[t * DK + lane * CH + c] : 0.0f;
+      qt[c] = on ? Q[t * DK + lane * CH + c] : 0.0f;
+      d[c] = 1.0f;
+    }
+    int s = t;
+    while (true) {
+      float kk = 0.0f, qk = 0.0f;
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const float x = on ? d[c] * K[s * DK + lane * CH + c] : 0.0f;
+        kk = fmaf(kt[c], x, kk);
+        qk = fmaf(qt[c], x, qk);
+      }
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) {
+        kk += __shfl_xor_sync(0xffffffffu, kk, off);
+        qk += __shfl_xor_sync(0xffffffffu, qk, off);
+      }
+      if (lane == 0) {
+        KK[t * rows + s] = kk;
+        QK[t * rows + s] = qk;
+      }
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        if constexpr (KDA) {
+          if (on) d[c] *= __ldg(p.g + ((int64_t)(c0 + s) * H + h) * DK + lane * CH + c);
+        } else {
+          d[c] *= gate[s];
+        }
+      }
+      s = par[s];
+      if (s < 0) break;
+    }
+    if constexpr (KDA) {
+      if (on) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          KG[t * DK + lane * CH + c] = kt[c] * d[c];
+          Q[t * DK + lane * CH + c] = qt[c] * d[c];  // read by this warp only
+        }
+      }
+    } else if (lane == 0) {
+      gamma[t] = d[0];
+    }
+  }
+  __syncthreads();
+
+  TileReader<ST> S;
+  S.init(p.src, (int64_t)slot * H + h, DK, DV, p.src_n_hp, row_info);
+  const float* KS = KDA ? KG : K;
+  constexpr int NPT = kBlock * DV / kTreeThreads;  // nodes of a thread in one pass
+  const int j = tid % DV, grp = tid / DV;
+  for (int t0 = 0; t0 < n; t0 += kBlock) {
+    float ak[NPT], aq[NPT];
+#pragma unroll
+    for (int m = 0; m < NPT; ++m) ak[m] = aq[m] = 0.0f;
+    for (int i = 0; i < DK; i += 4) {
+      float s[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[e] = S.template at<DV>(i + e, j);
+#pragma unroll
+      for (int m = 0; m < NPT; ++m) {
+        const float4 kk = *reinterpret_cast<const float4*>(KS + (t0 + grp * NPT + m) * DK + i);
+        const float4 qq = *reinterpret_cast<const float4*>(Q + (t0 + grp * NPT + m) * DK + i);
+        ak[m] = fmaf(kk.x, s[0], fmaf(kk.y, s[1], fmaf(kk.z, s[2], fmaf(kk.w, s[3], ak[m]))));
+        aq[m] = fmaf(qq.x, s[0], fmaf(qq.y, s[1], fmaf(qq.z, s[2], fmaf(qq.w, s[3], aq[m]))));
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < NPT; ++m) {
+      buf[(2 * (grp * NPT + m)) * DV + j] = ak[m];
+      buf[(2 * (grp * NPT + m) + 1) * DV + j] = aq[m];
+    }
+    __syncthreads();
+    if (tid < DV) {
+      for (int t = t0; t < min(t0 + kBlock, n); ++t) {
+        const float G = KDA ? 1.0f : gamma[t];
+        float pred = G * buf[(2 * (t - t0)) * DV + j], out = G * buf[(2 * (t - t0) + 1) * DV + j];
+        for (int s = par[t]; s >= 0; s = par[s]) {
+          pred = fmaf(KK[t * rows + s], U[s * DV + j], pred);
+          out = fmaf(QK[t * rows + s], U[s * DV + j], out);
+        }
+        const int64_t at = ((int64_t)(c0 + t) * H + h) * DV + j;
+        float x = io_load(gv + at);
+        if (p.predicts) x -= pred;
+        if (p.use_beta) x *= __ldg(p.beta + (int64_t)(c0 + t) * H + h);
+        U[t * DV + j] = x;
+        if (p.u) p.u[at] = x;
+        io_store(static_cast<IT*>(p.o) + at, p.scale * fmaf(QK[t * rows + t], x, out));
+      }
+    }
+    __syncthreads();
+  }
+}
+
+template <typename ST, typename IT, int DK, int DV, bool KDA>
+cudaError_t launch_tree(const TreeParams& p, cudaStream_t stream) {
+  const int rows = (p.max_nodes + kBlock - 1) / kBlock * kBlock;
+  auto fn = &tree_kernel<ST, IT, DK, DV, KDA>;
+  if (prepare_kernel(reinterpret_cast<const void*>(fn), kTreeThreads, tree_smem<DK, DV>(kMaxNodes, KDA)) <= 0)
+    return cudaErrorInvalidConfiguration;
+  fn<<<p.n_seqs * p.n_v_heads, kTreeThreads, tree_smem<DK, DV>(rows, KDA), stream>>>(p, rows);
+  return cudaGetLastError();
+}
+
+// ---- commit ------------------------------------------------------------------------------------
+// S <- Gamma_leaf S0 + sum over the path's nodes s of (D_leaf,s k_s) u_s^T, rounded once at the
+// store.  One CTA per (sequence, state head), one column of d_v per thread.
+
+template <int DK, int DV>
+__host__ __device__ constexpr int commit_smem(int rows) {
+  return 4 * (rows * (DK + DV) + DK + 2 * DK + rows);
+}
+
+template <typename ST, typename IT, int DK, int DV, bool KDA>
+__global__ void __launch_bounds__(DV < 32 ? 32 : DV) commit_kernel(const TreeCommitParams p, int rows) {
+  extern __shared__ __align__(16) float sm[];
+  float* kc = sm;                 // [path][DK]: D_leaf,s k_s
+  float* us = kc + rows * DK;     // [path][DV]
+  float* G = us + rows * DV;      // [DK]
+  int* src_info = reinterpret_cast<int*>(G + DK);  // [DK] (q8)
+  int* dst_info = src_info + DK;
+  int* path = dst_info + DK;      // [rows]: leaf first
+  __shared__ int n_path;
+  const int H = p.n_v_heads;
+  const int b = blockIdx.x / H, h = blockIdx.x % H;
+  const int hq = h / (H / p.n_qk_heads);
+  const int tid = threadIdx.x, NT = blockDim.x;
+  int c0;
+  const int n = tree_span(p.cu, p.total, p.max_nodes, b, c0);
+  if (n < 0) {
+    if (tid == 0) report(p.err, span_error(n));
+    return;
+  }
+  const int rs = p.read_slot ? __ldg(p.read_slot + b) : b, ws = p.write_slot ? __ldg(p.write_slot + b) : b;
+  const bool r_ok = rs >= 0 && rs < p.src_slots, w_ok = ws >= 0 && ws < p.dst_slots;
+  if (!r_ok || !w_ok) {
+    if (tid == 0) report(p.err, (r_ok ? 0u : LA_DEVERR_READ_SLOT) | (w_ok ? 0u : LA_DEVERR_WRITE_SLOT));
+    return;
+  }
+  if (tid == 0) {
+    int m = 0, s = __ldg(p.leaf + b);
+    bool ok = s >= -1 && s < n;
+    while (ok && s >= 0) {
+      path[m++] = s;
+      const int up = __ldg(p.parent + c0 + s);
+      ok = up >= -1 && up < s;
+      s = up;
+    }
+    n_path = ok ? m : -1;
+  }
+  __syncthreads();
+  const int m = n_path;
+  if (m < 0) {
+    if (tid == 0) report(p.err, LA_DEVERR_TREE);
+    return;
+  }
+  constexpr bool Q8 = sizeof(ST) == sizeof(q8_t);
+  if constexpr (Q8) {
+    if (!q8_rows(p.src_mask + h * (DK / 32), DK, p.n_hp, src_info) ||
+        !q8_rows(p.dst_mask + h * (DK / 32), DK, p.n_hp, dst_info)) {
+      if (tid == 0) report(p.err, LA_DEVERR_Q8_MASK);
+      return;
+    }
+    if (m == 0 && p.src_mask == p.dst_mask) {  // nothing accepted: the tile as it is
+      const int64_t bytes = q8_tile_bytes(DK, DV, p.n_hp);
+      const uint4* s = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(p.src) + ((int64_t)rs * H + h) * bytes);
+      uint4* d = reinterpret_cast<uint4*>(static_cast<unsigned char*>(p.dst) + ((int64_t)ws * H + h) * bytes);
+      for (int i = tid; i < bytes / 16; i += NT) d[i] = s[i];
+      return;
+    }
+  }
+  const IT* gk = static_cast<const IT*>(p.k);
+  for (int i = tid; i < DK; i += NT) {
+    float d = 1.0f;
+    for (int a = 0; a < m; ++a) {
+      const int64_t t = c0 + path[a];
+      kc[a * DK + i] = d * io_load(gk + (t * p.n_qk_heads + hq) * DK + i);
+      if (p.g) d *= KDA ? __ldg(p.g + (t * H + h) * DK + i) : __ldg(p.g + t * H + h);
+    }
+    G[i] = d;
+  }
+  for (int e = tid; e < m * DV; e += NT)
+    us[e] = __ldg(p.u + ((int64_t)(c0 + path[e / DV]) * H + h) * DV + e % DV);
+  __syncthreads();
+  TileReader<ST> S;
+  S.init(p.src, (int64_t)rs * H + h, DK, DV, p.n_hp, src_info);
+  const int j = tid;
+  if (j >= DV) return;
+  for (int i = 0; i < DK; ++i) {
+    float x = S.template at<DV>(i, j);
+    if (m > 0) x *= G[i];
+    for (int a = 0; a < m; ++a) x = fmaf(kc[a * DK + i], us[a * DV + j], x);
+    if constexpr (Q8) {
+      constexpr int NG = DV / 32;
+      const int n8 = DK - p.n_hp, e = dst_info[i], idx = e >> 1;
+      unsigned char* tile = static_cast<unsigned char*>(p.dst) + ((int64_t)ws * H + h) * q8_tile_bytes(DK, DV, p.n_hp);
+      float amax = fabsf(x);
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+      if (e & 1) {
+        reinterpret_cast<__nv_bfloat16*>(tile + n8 * DV + n8 * NG * 4)[idx * DV + j] = __float2bfloat16_rn(x);
+      } else {
+        float s, inv;
+        q8_scales(amax, s, inv);
+        reinterpret_cast<int8_t*>(tile)[idx * DV + j] = (int8_t)(int)q8_code(x, inv);
+        if ((j & 31) == 0) reinterpret_cast<float*>(tile + n8 * DV)[idx * NG + (j >> 5)] = s;
+      }
+    } else {
+      io_store(static_cast<ST*>(p.dst) + ((int64_t)ws * H + h) * DK * DV + i * DV + j, x);
+    }
+  }
+}
+
+template <typename ST, typename IT, int DK, int DV, bool KDA>
+cudaError_t launch_commit(const TreeCommitParams& p, cudaStream_t stream) {
+  auto fn = &commit_kernel<ST, IT, DK, DV, KDA>;
+  constexpr int kThreads = DV < 32 ? 32 : DV;
+  if (prepare_kernel(reinterpret_cast<const void*>(fn), kThreads, commit_smem<DK, DV>(kMaxNodes)) <= 0)
+    return cudaErrorInvalidConfiguration;
+  fn<<<p.n_seqs * p.n_v_heads, kThreads, commit_smem<DK, DV>(p.max_nodes), stream>>>(p, p.max_nodes);
+  return cudaGetLastError();
+}
+
+}  // namespace tree
+}  // namespace la

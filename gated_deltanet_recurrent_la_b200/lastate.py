@@ -26,6 +26,8 @@ STATUS = {0: "LA_OK", 1: "LA_ERR_NULL", 2: "LA_ERR_SHAPE", 3: "LA_ERR_UNSUPPORTE
           5: "LA_ERR_ALIAS", 6: "LA_ERR_CUDA"}
 LA_OK, LA_ERR_NULL, LA_ERR_SHAPE, LA_ERR_UNSUPPORTED, LA_ERR_ALIGN, LA_ERR_ALIAS, LA_ERR_CUDA = range(7)
 DEVERR_READ_SLOT, DEVERR_WRITE_SLOT, DEVERR_CU_SEQLENS, DEVERR_TIMEOUT, DEVERR_Q8_MASK = 1, 2, 4, 8, 16
+DEVERR_TREE, DEVERR_NO_SLOT, DEVERR_REF = 32, 64, 128
+TREE_MAX_NODES, BEAM_MAX, MAX_SLABS = 64, 64, 128
 
 EXPORTS = ("la_state_bytes", "la_shape_supported", "la_state_step", "la_state_scan", "la_state_scan_chunked",
            "la_state_scan_checkpointed", "la_state_scan_chunked_checkpointed", "la_state_step_qgroups",
@@ -38,7 +40,10 @@ EXPORTS = ("la_state_bytes", "la_shape_supported", "la_state_step", "la_state_sc
            "la_state_pool_copy",
            "la_state_pool_gather", "la_state_pool_scatter", "la_state_pool_zero", "la_state_check_slots",
            "la_status_str", "la_last_cuda_error", "la_abi_version", "la_debug_set_wait_limit_us",
-           "la_debug_withhold_step_tile")
+           "la_debug_withhold_step_tile",
+           "la_state_tree", "la_tree_accept", "la_state_tree_commit", "la_beam_workspace_bytes", "la_beam_select",
+           "la_pool_slab", "la_state_pool_reorder", "la_state_pool_alloc", "la_state_pool_share", "la_state_pool_free",
+           "la_state_pool_fork", "la_state_pool_compact", "la_state_pool_remap")
 
 
 class LAError(RuntimeError):
@@ -58,6 +63,10 @@ class la_shape(ctypes.Structure):
 class la_pool(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("n_slots", ctypes.c_int32),
                 ("shape", la_shape), ("n_hp", ctypes.c_int32), ("hp_mask", ctypes.c_void_p)]
+
+
+class la_slab(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("slot_bytes", ctypes.c_int64), ("n_slots", ctypes.c_int32)]
 
 
 class la_conv(ctypes.Structure):
@@ -142,6 +151,25 @@ def lib():
         L.la_debug_set_wait_limit_us.restype = None
         L.la_debug_withhold_step_tile.argtypes = [I32]
         L.la_debug_withhold_step_tile.restype = None
+        I64, Z, PS = ctypes.c_int64, ctypes.c_size_t, ctypes.POINTER(la_slab)
+        L.la_state_tree.argtypes = [I32, PP, P, I32, P, I32, P, I32, P, P, P, I32, P, P, F, P, P, P, P]
+        L.la_tree_accept.argtypes = [I32, P, I32, P, I32, P, P, P, P, P, P, P, P]
+        L.la_state_tree_commit.argtypes = [I32, PP, P, PP, P, I32, P, I32, P, P, I32, P, I32, P, P, P, P]
+        L.la_beam_workspace_bytes.argtypes = [I32, I32, I32, I32]
+        L.la_beam_workspace_bytes.restype = Z
+        L.la_beam_select.argtypes = [I32, I32, I32, P, I32, I64, P, P, I32, I32, P, P, P, P, P, Z, P]
+        L.la_pool_slab.argtypes = [PP, PS]
+        L.la_state_pool_reorder.argtypes = [PS, I32, I32, I32, P, P, P, P, P]
+        L.la_state_pool_alloc.argtypes = [P, I32, I32, P, P, P]
+        L.la_state_pool_share.argtypes = L.la_state_pool_alloc.argtypes
+        L.la_state_pool_free.argtypes = L.la_state_pool_alloc.argtypes
+        L.la_state_pool_fork.argtypes = [PS, I32, P, I32, P, P, P, P]
+        L.la_state_pool_compact.argtypes = [PS, I32, P, P, P, P, P, P, P]
+        L.la_state_pool_remap.argtypes = [I64, P, I32, P, P, P, P]
+        for f in (L.la_state_tree, L.la_tree_accept, L.la_state_tree_commit, L.la_beam_select, L.la_pool_slab,
+                  L.la_state_pool_reorder, L.la_state_pool_alloc, L.la_state_pool_share, L.la_state_pool_free,
+                  L.la_state_pool_fork, L.la_state_pool_compact, L.la_state_pool_remap):
+            f.restype = I32
         _lib = L
     return _lib
 
@@ -489,3 +517,141 @@ def la_debug_withhold_step_tile(tile: int) -> None:
     """Test hook: the next decode step on this thread withholds one tile's arrival, so its
     waits run out and LA_DEVERR_TIMEOUT is reported (nothing is left in flight)."""
     lib().la_debug_withhold_step_tile(int(tile))
+
+
+# ---- drafted token trees --------------------------------------------------------------------
+
+
+def la_state_tree(rule, src: Pool, read_slot, cu_nodes, parent, max_nodes: int, q, k, v, g, beta, scale, o, u, err_word,
+                  stream=None) -> int:
+    """Outputs o [T, H_v, d_v] (and write vectors u, float32, or None) of the packed drafted
+    trees below the pool's states; parent int32 [T], cu_nodes int32 [n_seqs + 1]."""
+    io = dtype_code(q.dtype)
+    return lib().la_state_tree(RULES[rule] if isinstance(rule, str) else int(rule), src.ref,
+                               _ptr(read_slot, torch.int32), int(cu_nodes.numel() - 1), _ptr(cu_nodes, torch.int32),
+                               int(q.shape[0]), _ptr(parent, torch.int32), int(max_nodes), _ptr(q), _ptr(k, q.dtype),
+                               _ptr(v, q.dtype), io, _ptr(g, torch.float32), _ptr(beta, torch.float32), float(scale),
+                               _ptr(o, q.dtype), _ptr(u, torch.float32), _ptr(err_word, torch.int32), _stream(stream))
+
+
+def la_tree_accept(cu_nodes, parent, max_nodes: int, draft, target, root, leaf, count, next_token, err_word,
+                   stream=None) -> int:
+    """The accepted path of every drafted tree: its last node, its length, the token behind it."""
+    i32 = torch.int32
+    return lib().la_tree_accept(int(cu_nodes.numel() - 1), _ptr(cu_nodes, i32), int(parent.numel()), _ptr(parent, i32),
+                                int(max_nodes), _ptr(draft, i32), _ptr(target, i32), _ptr(root, i32), _ptr(leaf, i32),
+                                _ptr(count, i32), _ptr(next_token, i32), _ptr(err_word, i32), _stream(stream))
+
+
+def la_state_tree_commit(rule, src: Pool, read_slot, dst: Pool, write_slot, cu_nodes, parent, leaf, max_nodes: int, k, g, u,
+                         err_word, stream=None) -> int:
+    """The state after each sequence's node leaf[b], from the write vectors la_state_tree kept."""
+    io = dtype_code(k.dtype)
+    return lib().la_state_tree_commit(RULES[rule] if isinstance(rule, str) else int(rule), src.ref,
+                                      _ptr(read_slot, torch.int32), dst.ref, _ptr(write_slot, torch.int32),
+                                      int(cu_nodes.numel() - 1), _ptr(cu_nodes, torch.int32), int(k.shape[0]),
+                                      _ptr(parent, torch.int32), _ptr(leaf, torch.int32), int(max_nodes), _ptr(k), io,
+                                      _ptr(g, torch.float32), _ptr(u, torch.float32), _ptr(err_word, torch.int32),
+                                      _stream(stream))
+
+
+# ---- beam search ----------------------------------------------------------------------------
+
+
+def la_beam_workspace_bytes(n_seqs: int, n_beams: int, vocab: int, n_out: int) -> int:
+    return lib().la_beam_workspace_bytes(int(n_seqs), int(n_beams), int(vocab), int(n_out))
+
+
+def la_beam_select(logits, cum_score, finished, eos_token: int, parent, token, score, finished_out, workspace,
+                   stream=None) -> int:
+    """The best parent.shape[1] continuations of every sequence: logits [n_seqs, n_beams, vocab]
+    (rows may be further apart than vocab, as those of a slice), cum_score float32 [n_seqs,
+    n_beams], finished int32 or None; workspace: la_beam_workspace_bytes(...) uint8."""
+    B, K, V = logits.shape
+    stride = logits.stride(1) if K > 1 else logits.stride(0) if B > 1 else V
+    if not logits.is_cuda:
+        raise ValueError("tensor must live on a CUDA device")
+    if (V > 1 and logits.stride(2) != 1) or (B > 1 and K > 1 and logits.stride(0) != K * stride):
+        raise ValueError("logits must be rows of contiguous values, equally far apart")
+    i32 = torch.int32
+    return lib().la_beam_select(B, K, V, ctypes.c_void_p(logits.data_ptr()), dtype_code(logits.dtype), int(stride),
+                                _ptr(cum_score, torch.float32), _ptr(finished, i32), int(eos_token),
+                                int(parent.shape[1]), _ptr(parent, i32), _ptr(token, i32), _ptr(score, torch.float32),
+                                _ptr(finished_out, i32), _ptr(workspace), int(workspace.numel() * workspace.element_size()),
+                                _stream(stream))
+
+
+# ---- slots over all layers ------------------------------------------------------------------
+
+
+class Slabs:
+    """The arrays a slot index points into, over all layers: Pools of any dtype, and tensors
+    [n_slots, ...] such as convolution histories."""
+
+    def __init__(self, arrays):
+        self.keep = list(arrays)
+        self.n = len(self.keep)
+        self.array = (la_slab * max(1, self.n))()
+        for i, a in enumerate(self.keep):
+            if isinstance(a, Pool):
+                check(lib().la_pool_slab(a.ref, ctypes.byref(self.array[i])))
+            else:
+                n_slots = int(a.shape[0])
+                self.array[i] = la_slab(_ptr(a), a.numel() // max(1, n_slots) * a.element_size(), n_slots)
+
+    @property
+    def n_slots(self) -> int:
+        return int(self.array[0].n_slots)
+
+
+def la_state_pool_reorder(slabs: Slabs, slots, parent, new_slots, err_word, stream=None) -> int:
+    """slots, parent, new_slots int32 [n_seqs, n_beams]: new beam j continues old beam parent[b, j]."""
+    i32 = torch.int32
+    return lib().la_state_pool_reorder(slabs.array, slabs.n, int(slots.shape[0]), int(slots.shape[1]), _ptr(slots, i32),
+                                       _ptr(parent, i32), _ptr(new_slots, i32), _ptr(err_word, i32), _stream(stream))
+
+
+def la_state_pool_alloc(ref, slots, err_word, stream=None) -> int:
+    """slots <- the lowest free slots (ref 0), their count 1; -1 where there are no more."""
+    i32 = torch.int32
+    return lib().la_state_pool_alloc(_ptr(ref, i32), int(ref.numel()), int(slots.numel()), _ptr(slots, i32),
+                                     _ptr(err_word, i32), _stream(stream))
+
+
+def la_state_pool_share(ref, slots, err_word, stream=None) -> int:
+    """One more holder of each slot."""
+    i32 = torch.int32
+    return lib().la_state_pool_share(_ptr(ref, i32), int(ref.numel()), int(slots.numel()), _ptr(slots, i32),
+                                     _ptr(err_word, i32), _stream(stream))
+
+
+def la_state_pool_free(ref, slots, err_word, stream=None) -> int:
+    """One holder less of each slot; at 0 it is free."""
+    i32 = torch.int32
+    return lib().la_state_pool_free(_ptr(ref, i32), int(ref.numel()), int(slots.numel()), _ptr(slots, i32),
+                                    _ptr(err_word, i32), _stream(stream))
+
+
+def la_state_pool_fork(slabs: Slabs, ref, src_slots, new_slots, err_word, stream=None) -> int:
+    """new_slots <- allocated slots holding copies of src_slots in every slab."""
+    i32 = torch.int32
+    if ref.numel() != slabs.n_slots or new_slots.numel() != src_slots.numel():
+        raise ValueError("ref has one count per slot, new_slots one slot per source")
+    return lib().la_state_pool_fork(slabs.array, slabs.n, _ptr(ref, i32), int(src_slots.numel()), _ptr(src_slots, i32),
+                                    _ptr(new_slots, i32), _ptr(err_word, i32), _stream(stream))
+
+
+def la_state_pool_compact(slabs: Slabs, ref, new_ref, remap, moves, counts, err_word, stream=None) -> int:
+    """Live slots to the front of every slab; new_ref, remap, moves int32 [n_slots], counts int32 [2]."""
+    i32 = torch.int32
+    if any(t.numel() != slabs.n_slots for t in (ref, new_ref, remap, moves)) or counts.numel() < 2:
+        raise ValueError("ref, new_ref, remap and moves have one entry per slot, counts two")
+    return lib().la_state_pool_compact(slabs.array, slabs.n, _ptr(ref, i32), _ptr(new_ref, i32), _ptr(remap, i32),
+                                       _ptr(moves, i32), _ptr(counts, i32), _ptr(err_word, i32), _stream(stream))
+
+
+def la_state_pool_remap(table, remap, new_table, err_word, stream=None) -> int:
+    """new_table[i] <- remap[table[i]]; -1 stays."""
+    i32 = torch.int32
+    return lib().la_state_pool_remap(int(table.numel()), _ptr(table, i32), int(remap.numel()), _ptr(remap, i32),
+                                     _ptr(new_table, i32), _ptr(err_word, i32), _stream(stream))

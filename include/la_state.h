@@ -81,7 +81,7 @@
 extern "C" {
 #endif
 
-#define LA_ABI_VERSION 4
+#define LA_ABI_VERSION 5
 
 typedef enum {
     LA_RULE_LINEAR = 0,
@@ -110,6 +110,10 @@ typedef enum {
 #define LA_DEVERR_CU_SEQLENS 4u /* cu_seqlens not non-decreasing within [0, total_tokens], or a bad seq_order entry */
 #define LA_DEVERR_TIMEOUT 8u    /* an internal pipeline wait gave up (should never happen) */
 #define LA_DEVERR_Q8_MASK 16u   /* a q8 head's channel mask does not hold exactly n_hp rows */
+#define LA_DEVERR_TREE 32u      /* a tree with a parent not before its child, more nodes than max_nodes or a
+                                   leaf outside it; a beam's parent outside [0, n_beams) */
+#define LA_DEVERR_NO_SLOT 64u   /* fewer free slots than asked for */
+#define LA_DEVERR_REF 128u      /* a slot shared or freed that nothing holds */
 
 typedef struct {
     int32_t n_qk_heads; /* H_qk: heads of q and k */
@@ -469,6 +473,143 @@ la_status la_state_pool_encode(const la_pool *pool, int32_t n, const int32_t *sl
                                const float *dense, int32_t *err_word, void *stream);
 la_status la_state_pool_decode(const la_pool *pool, int32_t n, const int32_t *slots, float *dense,
                                int32_t *err_word, void *stream);
+
+/* ---- drafted token trees (speculative decoding) -----------------------------------------
+ *
+ * A request's drafted tokens form a tree below its current state ("Seven Architectures ...",
+ * Limitations: branch-local state for a tree of drafted tokens).  The nodes of sequence b are
+ * the packed rows [cu_nodes[b], cu_nodes[b + 1]); parent[t] is the place of node t's parent
+ * within its sequence, -1 for a node that follows the sequence's last token, and lies before
+ * t.  Every node's state continues its parent's by the rule, S_t = a_t S_p + k_t u_t^T, but
+ * no state is stored: la_state_tree reads the pool once and returns each node's output
+ * o_t = scale S_t^T q_t and, for a later commit, its write vector u_t.
+ *   src, read_slot  the current states: src slot read_slot[b] (NULL: slot b); any dtype
+ *   cu_nodes        device int32 [n_seqs + 1];  total_nodes: the leading size of the arrays
+ *   parent          device int32 [total_nodes]
+ *   max_nodes       the most nodes a sequence of this call has, 1 .. LA_TREE_MAX_NODES (it sizes the
+ *                   kernel; a sequence with more is skipped with LA_DEVERR_TREE)
+ *   q, k            [total_nodes, H_qk, d_k];  v, o: [total_nodes, H_v, d_v] (io dtype);
+ *   g, beta         as la_state_scan
+ *   u               device float32 [total_nodes, H_v, d_v], 16-byte aligned, or NULL
+ * A sequence without nodes is left alone.  Gates of zero and of either sign are exact (decays
+ * are products along the path, never ratios), and a non-finite value reaches only the nodes
+ * below it.  FP32 arithmetic; host errors as la_state_step (LA_ERR_UNSUPPORTED for max_nodes
+ * above LA_TREE_MAX_NODES, LA_ERR_SHAPE below 1). */
+#define LA_TREE_MAX_NODES 64
+la_status la_state_tree(la_rule rule, const la_pool *src, const int32_t *read_slot, int32_t n_seqs,
+                        const int32_t *cu_nodes, int32_t total_nodes, const int32_t *parent,
+                        int32_t max_nodes, const void *q, const void *k, const void *v, la_dtype io,
+                        const float *g, const float *beta, float scale, void *o, float *u,
+                        int32_t *err_word, void *stream);
+
+/* The drafted path the target model agrees with: from the root, the lowest child whose drafted
+ * token is the one the target wants there, as far as it goes.
+ *   draft    device int32 [total_nodes]: the nodes' drafted tokens
+ *   target   device int32 [total_nodes]: the target's token after each node;  root: [n_seqs], its
+ *            token after the sequence's last one
+ *   leaf     device int32 [n_seqs]: the last accepted node (its place in the sequence), -1 for none
+ *   count    device int32 [n_seqs]: nodes accepted;  next: [n_seqs]: the target's token behind them
+ * The results of a sequence with a bad tree stay as they were (LA_DEVERR_TREE). */
+la_status la_tree_accept(int32_t n_seqs, const int32_t *cu_nodes, int32_t total_nodes,
+                         const int32_t *parent, int32_t max_nodes, const int32_t *draft,
+                         const int32_t *target, const int32_t *root, int32_t *leaf, int32_t *count,
+                         int32_t *next, int32_t *err_word, void *stream);
+
+/* The state after node leaf[b] of every sequence, from the write vectors la_state_tree kept:
+ *   S <- Gamma_leaf S + sum over the path's nodes s of (D_leaf,s k_s) u_s^T
+ * (Gamma, D: products of the gates along the path), read at src slot read_slot[b] (NULL: slot b)
+ * and written at dst slot write_slot[b] (NULL: slot b), rounded once.  leaf[b] == -1: the state is
+ * copied.  A sequence may read and write one slot.  src and dst have one shape and dtype (q8:
+ * equal n_hp; LA_ERR_ALIAS for one pool with two mask arrays).  linear and gated rules take u
+ * from la_state_tree too (there u = v).  g as la_state_tree (ignored by linear and delta). */
+la_status la_state_tree_commit(la_rule rule, const la_pool *src, const int32_t *read_slot,
+                               const la_pool *dst, const int32_t *write_slot, int32_t n_seqs,
+                               const int32_t *cu_nodes, int32_t total_nodes, const int32_t *parent,
+                               const int32_t *leaf, int32_t max_nodes, const void *k, la_dtype io,
+                               const float *g, const float *u, int32_t *err_word, void *stream);
+
+/* ---- beam search ---------------------------------------------------------------------------
+ *
+ * The n_out best continuations of every sequence over its beams i and the vocabulary, by
+ *   cum_score[b, i] + x_v - logsumexp(x),   x the logits of beam i,
+ * best first, ties to the lower (i, v).
+ *   logits      device, io dtype: beam i of sequence b is row b * n_beams + i, row_stride elements
+ *               apart (>= vocab), any alignment of the element size
+ *   cum_score   device float32 [n_seqs, n_beams]; -inf: a beam that is not there (in a first
+ *               step all but one)
+ *   finished    device int32 [n_seqs, n_beams] or NULL; a finished beam (!= 0) has one
+ *               continuation, eos_token, at its own score (0 <= eos_token < vocab then)
+ *   parent, token   device int32 [n_seqs, n_out];  score: float32;  finished_out: int32 or NULL,
+ *               set where the parent was finished or the token is eos_token
+ *   workspace   device, 16-byte aligned, at least la_beam_workspace_bytes(...); scratch
+ * Logits of -inf are masked tokens, NaN counts as -inf and +inf as the largest float.  Scores are
+ * formed and compared in FP64 and rounded once.  n_beams, n_out in 1 .. LA_BEAM_MAX
+ * (LA_ERR_UNSUPPORTED above), n_out <= n_beams * vocab (LA_ERR_SHAPE).  n_seqs == 0 is a no-op. */
+#define LA_BEAM_MAX 64
+size_t la_beam_workspace_bytes(int32_t n_seqs, int32_t n_beams, int32_t vocab, int32_t n_out);
+la_status la_beam_select(int32_t n_seqs, int32_t n_beams, int32_t vocab, const void *logits, la_dtype io,
+                         int64_t row_stride, const float *cum_score, const int32_t *finished,
+                         int32_t eos_token, int32_t n_out, int32_t *parent, int32_t *token,
+                         float *score, int32_t *finished_out, void *workspace, size_t workspace_bytes,
+                         void *stream);
+
+/* ---- slots over all layers --------------------------------------------------------------------
+ *
+ * A request holds one slot index in the state pools and convolution histories of every layer.  A
+ * slab is one of those arrays: n_slots slots of slot_bytes each, contiguous (la_pool_slab makes
+ * one of a pool of any dtype; a history is [n_slots] x H_v (2 d_k + d_v) (W - 1) elements).  The
+ * slabs of a call (a HOST array, read before the call returns) have one n_slots, slot_bytes a
+ * multiple of 16 and 16-byte aligned data, and do not overlap; 1 .. LA_MAX_SLABS of them.
+ * ("Recurrent state" glossary: slots allocated per active request, compaction, read and write
+ * slots of a prefix-cache checkpoint.)  Copies are bit copies.
+ *   reorder   beam search: new beam j of sequence b continues old beam parent[b, j].  The first
+ *             child of a beam keeps its slot, every other child gets the slot of a beam without
+ *             children and a copy of its parent's states: new_slots[b, j] (both in increasing
+ *             order; the slots of a sequence stay the same set).  slots, parent, new_slots: device
+ *             int32 [n_seqs, n_beams], n_beams <= LA_BEAM_MAX; slots distinct; new_slots another
+ *             array than slots (LA_ERR_ALIAS).  A sequence with a bad slot or parent is left as it
+ *             is, its new_slots -1.
+ * With reference counts, ref: device int32 [n_slots], 0 = free:
+ *   alloc     slots[0 .. n) <- the n lowest free slots in increasing order, their count 1; where
+ *             there are fewer, -1 and LA_DEVERR_NO_SLOT
+ *   share     count + 1 of each of the n slots (a slot may be there twice); of a free slot:
+ *             LA_DEVERR_REF, unchanged
+ *   free      count - 1, likewise.  A slot of -1 is passed over by both
+ *   fork      alloc, then new slot i holds a copy of src_slots[i] in every slab.  A source may be
+ *             there twice; one outside the pool (LA_DEVERR_READ_SLOT) or that nothing holds
+ *             (LA_DEVERR_REF) gets no slot (-1).  src_slots and new_slots are different arrays
+ *   compact   with n_live the number of slots with ref > 0: those at n_live or behind move to the
+ *             free ones before it, both in increasing order, in every slab; slots from n_live on
+ *             are then free.  ref is read; new_ref [n_slots]: the counts after it; remap [n_slots]:
+ *             each live slot's new place, -1 for a free one; moves [n_slots]: the old places of
+ *             those that moved, in order, then -1; counts [2]: n_live and the number that moved.
+ *             Five different arrays (LA_ERR_ALIAS)
+ *   remap     new_table[i] <- remap[table[i]] (table may be new_table); -1 stays, a slot outside
+ *             [0, n_slots) stays and reports LA_DEVERR_READ_SLOT
+ * Calls on the same arrays are ordered by the caller (one stream). */
+#define LA_MAX_SLABS 128
+typedef struct {
+    void *data;         /* device, 16-byte aligned */
+    int64_t slot_bytes; /* a multiple of 16 */
+    int32_t n_slots;
+} la_slab;
+la_status la_pool_slab(const la_pool *pool, la_slab *slab);
+la_status la_state_pool_reorder(const la_slab *slabs, int32_t n_slabs, int32_t n_seqs, int32_t n_beams,
+                                const int32_t *slots, const int32_t *parent, int32_t *new_slots,
+                                int32_t *err_word, void *stream);
+la_status la_state_pool_alloc(int32_t *ref, int32_t n_slots, int32_t n, int32_t *slots, int32_t *err_word,
+                              void *stream);
+la_status la_state_pool_share(int32_t *ref, int32_t n_slots, int32_t n, const int32_t *slots,
+                              int32_t *err_word, void *stream);
+la_status la_state_pool_free(int32_t *ref, int32_t n_slots, int32_t n, const int32_t *slots,
+                             int32_t *err_word, void *stream);
+la_status la_state_pool_fork(const la_slab *slabs, int32_t n_slabs, int32_t *ref, int32_t n,
+                             const int32_t *src_slots, int32_t *new_slots, int32_t *err_word, void *stream);
+la_status la_state_pool_compact(const la_slab *slabs, int32_t n_slabs, const int32_t *ref, int32_t *new_ref,
+                                int32_t *remap, int32_t *moves, int32_t *counts, int32_t *err_word,
+                                void *stream);
+la_status la_state_pool_remap(int64_t n, const int32_t *table, int32_t n_slots, const int32_t *remap,
+                              int32_t *new_table, int32_t *err_word, void *stream);
 
 /* Host-side check of the slot preconditions of la_state_step / la_state_scan on HOST
  * copies of the slot arrays (either may be NULL = identity): every index in [0, n_slots),
