@@ -3,6 +3,7 @@
 #pragma once
 
 #include "la_tree.cuh"
+#include "la_tree_tc.cuh"
 
 namespace la {
 namespace tree {
@@ -11,10 +12,12 @@ template <typename IT, bool KDA>
 TreeLaunchFn find_tree_io(int dk, int dv, int st) {
 #define LA_TREE_CASE(ST_CODE, ST, DK, DV) \
   if (st == ST_CODE && dk == DK && dv == DV) return &launch_tree<ST, IT, DK, DV, KDA>;
-#define LA_TREE_SHAPES(ST_CODE, ST)        \
-  LA_TREE_CASE(ST_CODE, ST, 64, 64)        \
-  LA_TREE_CASE(ST_CODE, ST, 128, 64)       \
-  LA_TREE_CASE(ST_CODE, ST, 128, 128)
+#define LA_TREE_TC(ST_CODE, ST, DK, DV) \
+  if (st == ST_CODE && dk == DK && dv == DV) return &launch_tree_tc<ST, IT, DK, DV, KDA>;
+#define LA_TREE_SHAPES(ST_CODE, ST)      \
+  LA_TREE_TC(ST_CODE, ST, 64, 64)        \
+  LA_TREE_TC(ST_CODE, ST, 128, 64)       \
+  LA_TREE_TC(ST_CODE, ST, 128, 128)
   LA_TREE_CASE(LA_F32, float, 16, 16)
   LA_TREE_CASE(LA_BF16, __nv_bfloat16, 16, 16)
   LA_TREE_SHAPES(LA_F32, float)
@@ -22,6 +25,7 @@ TreeLaunchFn find_tree_io(int dk, int dv, int st) {
   LA_TREE_SHAPES(LA_Q8, q8_t)
   return nullptr;
 #undef LA_TREE_SHAPES
+#undef LA_TREE_TC
 #undef LA_TREE_CASE
 }
 
