@@ -5,6 +5,14 @@
 // its logits alone (ties to the lower index), and the sequence's best n_out are among them.
 // Scores are formed and compared in FP64: neighbouring candidates can lie closer than an FP32
 // rounding of a sum of their size, and their order decides whole numbers.
+//
+// beam_row_kernel reads a row (or a part of it, where rows are few) once from memory: each
+// thread keeps its running maximum, the sum of exponentials below it, and the key of its best
+// element.  The threads form 128 groups; the n_out-th best of the groups' best elements is at
+// or below the row's n_out-th best element, and elements at or above it lie in n_out groups
+// only, so a second look (from L2) at those few per cent of the row finds every candidate:
+// n_out of them and a handful more, which are ranked by counting.  beam_merge_kernel joins the
+// sorted lists.  Bound by the logits' bytes; the exponentials take about as long at BF16.
 #include "la_device.cuh"
 #include "la_serving.h"
 
@@ -12,12 +20,26 @@ namespace la {
 
 namespace {
 
-constexpr int kRowThreads = 256;
+constexpr int kRowThreads = 512;
+constexpr int kGroups = 128;    // of threads tid, tid + 128, ..; at least LA_BEAM_MAX
+constexpr int kCand = 512;      // candidates kept of one part
+constexpr int kMaxParts = 16;
+static_assert(kGroups >= LA_BEAM_MAX && kCand <= kRowThreads && kRowThreads % kGroups == 0, "sizes");
 
-struct BeamRow {     // of one beam: the scores' offset cum - logsumexp, then n_out (logit, index) pairs
-  double offset;
+struct BeamPart {   // of one part of a row: then n_out keys (order of the logit, ~index), best first; 0 = none
+  double sum;       // of exp(x - top)
+  float top;
+  float pad;
 };
-__host__ __device__ constexpr int64_t beam_row_bytes(int n_out) { return 8 + 8 * (int64_t)n_out; }
+__host__ __device__ constexpr int64_t beam_part_bytes(int n_out) { return (int64_t)sizeof(BeamPart) + 8 * (int64_t)n_out; }
+
+// Parts of a row: enough of them for two CTAs per SM, of 4096 elements at least (below that the
+// merge costs more than the reading).
+int beam_parts(int64_t rows, int64_t vocab) {
+  int64_t s = (2 * 148 + rows - 1) / rows;
+  if (s > vocab / 4096) s = vocab / 4096;
+  return (int)(s < 1 ? 1 : s > kMaxParts ? kMaxParts : s);
+}
 
 // FP32 order as an unsigned key; -0 counts as +0, NaN as -inf, +inf as the largest finite value
 __device__ __forceinline__ float beam_clean(float x) { return fminf(fmaxf(x, -INFINITY), 3.402823466e38f) + 0.0f; }
@@ -28,91 +50,314 @@ __device__ __forceinline__ uint32_t beam_order(float x) {
 __device__ __forceinline__ float beam_value(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
+__device__ __forceinline__ uint64_t beam_key(float x, int v) {
+  return ((uint64_t)beam_order(x) << 32) | (0xffffffffu - (uint32_t)v);
+}
+
+// The 16-byte pieces of elements [lo, hi) of a row, whatever its alignment; the first and the
+// last piece are read element by element.
+template <typename IT>
+struct RowPieces {
+  static constexpr int E = 16 / (int)sizeof(IT);
+  const IT* x;
+  int lo, hi, first, n;  // index of piece 0's first element (may lie before lo), number of pieces
+  __device__ __forceinline__ RowPieces(const IT* row, int lo_, int hi_) : x(row), lo(lo_), hi(hi_) {
+    first = lo - (int)((reinterpret_cast<uintptr_t>(row + lo) & 15u) / sizeof(IT));
+    n = hi > lo ? (hi - first + E - 1) / E : 0;
+  }
+  __device__ __forceinline__ bool full(int j) const { return first + j * E >= lo && first + (j + 1) * E <= hi; }
+  __device__ __forceinline__ bool has(int v) const { return v >= lo && v < hi; }
+  __device__ __forceinline__ uint4 load(int j) const {
+    const int v0 = first + j * E;
+    if (full(j)) return __ldg(reinterpret_cast<const uint4*>(x + v0));
+    uint32_t w[4];
+    if constexpr (sizeof(IT) == 4) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = has(v0 + e) ? __float_as_uint(x[v0 + e]) : 0xff800000u;
+    } else {
+      const unsigned short* h = reinterpret_cast<const unsigned short*>(x);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        w[e] = (has(v0 + 2 * e) ? (uint32_t)h[v0 + 2 * e] : 0xff80u) |
+               (has(v0 + 2 * e + 1) ? (uint32_t)h[v0 + 2 * e + 1] : 0xff80u) << 16;
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  static __device__ __forceinline__ void values(const uint4& w, float* f) {
+    StateVec<IT>::unpack(w, f);
+#pragma unroll
+    for (int e = 0; e < E; ++e) f[e] = beam_clean(f[e]);
+  }
+};
 
 template <typename IT>
-__global__ void __launch_bounds__(kRowThreads) beam_row_kernel(const BeamParams p) {
-  const int row = blockIdx.x, tid = threadIdx.x;
+__global__ void __launch_bounds__(kRowThreads) beam_row_kernel(const BeamParams p, int parts) {
+  constexpr int E = RowPieces<IT>::E;
+  __shared__ uint64_t keys[kRowThreads];  // the threads' best, then the groups', then the candidates
+  __shared__ double sums[kRowThreads / 32];
+  __shared__ float tops[kRowThreads / 32];
+  __shared__ int winners[LA_BEAM_MAX];
+  __shared__ uint64_t tau;
+  __shared__ int n_win, n_cand;
+  griddep_launch_dependents();
+  const int row = blockIdx.x / parts, part = blockIdx.x % parts, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const float cum = p.cum[row];
   const bool dead = !(cum > -INFINITY);
   const bool done = p.finished && p.finished[row] != 0;
-  const IT* x = static_cast<const IT*>(p.logits) + (int64_t)row * p.row_stride;
-  auto value = [&](int v) {
-    if (dead) return -INFINITY;
-    if (done) return v == p.eos ? 0.0f : -INFINITY;
-    return beam_clean(io_load(x + v));
-  };
-  __shared__ uint64_t best[kRowThreads / 32];
-  __shared__ double sums[kRowThreads / 32];
-  unsigned char* out = static_cast<unsigned char*>(p.workspace) + row * beam_row_bytes(p.n_out);
+  unsigned char* out = static_cast<unsigned char*>(p.workspace) + (int64_t)blockIdx.x * beam_part_bytes(p.n_out);
+  uint64_t* best = reinterpret_cast<uint64_t*>(out + sizeof(BeamPart));
+  BeamPart* head = reinterpret_cast<BeamPart*>(out);
   const int take = min(p.n_out, p.vocab);
+  if (dead || done) {  // no logits: eos at the beam's own score, everything else -inf
+    for (int r = tid; r < take; r += kRowThreads) {
+      uint64_t k = 0;
+      if (part == 0) {
+        if (dead) k = beam_key(-INFINITY, r);
+        else k = r == 0 ? beam_key(0.0f, p.eos) : beam_key(-INFINITY, r - 1 < p.eos ? r - 1 : r);
+      }
+      best[r] = k;
+    }
+    if (tid == 0) *head = BeamPart{0.0, -INFINITY, 0.0f};
+    return;
+  }
+  const int span = (p.vocab + parts - 1) / parts, lo = part * span, hi = min(p.vocab, lo + span);
+  const RowPieces<IT> pieces(static_cast<const IT*>(p.logits) + (int64_t)row * p.row_stride, lo, hi);
+
+  float top = -INFINITY, at = -INFINITY;
+  int where = -1;
+  double sum = 0.0;
+  auto visit = [&](const uint4& w, int j) {
+    float f[E];
+    RowPieces<IT>::values(w, f);
+    float m = f[0];
+#pragma unroll
+    for (int e = 1; e < E; ++e) m = fmaxf(m, f[e]);
+    if (m > at || where < 0) {  // the first of the thread's largest elements
+      const int v0 = pieces.first + j * E;
+      int first = -1;
+#pragma unroll
+      for (int e = E - 1; e >= 0; --e)
+        if (f[e] == m && pieces.has(v0 + e)) first = v0 + e;
+      if (first >= 0) {
+        at = m;
+        where = first;
+      }
+    }
+    if (m > top) {
+      sum *= (double)expf(top - m);
+      top = m;
+    }
+    if (top > -INFINITY) {
+      float s = 0.0f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) s += expf(f[e] - top);
+      sum += (double)s;
+    }
+  };
+  int j = tid;
+  for (; j + 3 * kRowThreads < pieces.n; j += 4 * kRowThreads) {  // four pieces in flight
+    uint4 w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = pieces.load(j + e * kRowThreads);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) visit(w[e], j + e * kRowThreads);
+  }
+  for (; j < pieces.n; j += kRowThreads) visit(pieces.load(j), j);
+
+  keys[tid] = where < 0 ? 0ull : beam_key(at, where);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    const float t = __shfl_xor_sync(0xffffffffu, top, off);
+    const double s = __shfl_xor_sync(0xffffffffu, sum, off);
+    const float m = fmaxf(top, t);
+    if (m > -INFINITY) sum = sum * (double)expf(top - m) + s * (double)expf(t - m);
+    top = m;
+  }
+  if (lane == 0) {
+    tops[warp] = top;
+    sums[warp] = sum;
+  }
+  if (tid == 0) {
+    tau = 0ull;
+    n_cand = n_win = 0;
+  }
+  __syncthreads();
+  uint64_t mine = 0ull;
+  if (tid < kGroups) {
+#pragma unroll
+    for (int e = 0; e < kRowThreads / kGroups; ++e) mine = max(mine, keys[tid + e * kGroups]);
+  } else if (tid == kGroups) {
+    float m = tops[0];
+    for (int w = 1; w < kRowThreads / 32; ++w) m = fmaxf(m, tops[w]);
+    double s = 0.0;
+    if (m > -INFINITY)
+      for (int w = 0; w < kRowThreads / 32; ++w) s += sums[w] * (double)expf(tops[w] - m);
+    *head = BeamPart{s, m, 0.0f};
+  }
+  __syncthreads();
+  if (tid < kGroups) keys[tid] = mine;
+  __syncthreads();
+  if (tid < kGroups && mine) {
+    int rank = 0;
+#pragma unroll 8
+    for (int g = 0; g < kGroups; ++g) rank += keys[g] > mine;
+    if (rank < take) {
+      winners[rank] = tid;
+      atomicAdd(&n_win, 1);
+      if (rank == take - 1) tau = mine;
+    }
+  }
+  __syncthreads();
+  // (fewer groups than n_out: the part has no more than 64 pieces, and all of it is taken)
+  const uint64_t border = tau;
+  const int wins = n_win, per = (pieces.n + kGroups - 1) / kGroups;
+  for (int e = tid; e < wins * per; e += kRowThreads) {
+    const int jj = winners[e % wins] + e / wins * kGroups;
+    if (jj >= pieces.n) continue;
+    float f[E];
+    RowPieces<IT>::values(pieces.load(jj), f);
+#pragma unroll
+    for (int c = 0; c < E; ++c) {
+      const int v = pieces.first + jj * E + c;
+      const uint64_t k = beam_key(f[c], v);
+      if (pieces.has(v) && k >= border) {
+        const int i = atomicAdd(&n_cand, 1);
+        if (i < kCand) keys[i] = k;
+      }
+    }
+  }
+  __syncthreads();
+  const int cand = n_cand;
+  if (cand <= kCand) {
+    for (int r = cand + tid; r < take; r += kRowThreads) best[r] = 0ull;
+    if (tid < cand) {
+      const uint64_t k = keys[tid];
+      int rank = 0;
+      for (int i = 0; i < cand; ++i) rank += keys[i] > k;
+      if (rank < take) best[rank] = k;
+    }
+    return;
+  }
+  // Many of the best in few groups (values laid out with the groups' stride): one pass each.
   uint64_t last = ~0ull;
-  float top = -INFINITY;
   for (int r = 0; r < take; ++r) {
     uint64_t k = 0;
-    for (int v = tid; v < p.vocab; v += kRowThreads) {
-      const uint64_t c = ((uint64_t)beam_order(value(v)) << 32) | (0xffffffffu - (uint32_t)v);
-      if (c < last && c > k) k = c;
+    for (int q = tid; q < pieces.n; q += kRowThreads) {
+      float f[E];
+      RowPieces<IT>::values(pieces.load(q), f);
+#pragma unroll
+      for (int c = 0; c < E; ++c) {
+        const int v = pieces.first + q * E + c;
+        const uint64_t x = beam_key(f[c], v);
+        if (pieces.has(v) && x < last && x > k) k = x;
+      }
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) k = max(k, __shfl_xor_sync(0xffffffffu, k, off));
-    if ((tid & 31) == 0) best[tid >> 5] = k;
     __syncthreads();
-    k = best[0];
-    for (int w = 1; w < kRowThreads / 32; ++w) k = max(k, best[w]);
+    if (lane == 0) keys[warp] = k;
     __syncthreads();
-    if (r == 0) top = beam_value((uint32_t)(k >> 32));
-    if (tid == 0) reinterpret_cast<uint64_t*>(out + 8)[r] = k;
+    for (int w = 0; w < kRowThreads / 32; ++w) k = max(k, keys[w]);
+    if (tid == 0) best[r] = k;
     last = k;
-  }
-  double sum = 0.0;
-  if (!dead && !done && top > -INFINITY)
-    for (int v = tid; v < p.vocab; v += kRowThreads) sum += (double)expf(value(v) - top);
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-  if ((tid & 31) == 0) sums[tid >> 5] = sum;
-  __syncthreads();
-  if (tid == 0) {
-    sum = 0.0;
-    for (int w = 0; w < kRowThreads / 32; ++w) sum += sums[w];
-    double off = (double)fminf(cum, 3.402823466e38f);
-    if (dead) off = 0.0;
-    else if (!done && top > -INFINITY) off -= (double)top + log(sum);
-    reinterpret_cast<BeamRow*>(out)->offset = off;
   }
 }
 
-// One CTA per sequence: every beam's list is in order, so a candidate's rank is the number of
-// better ones in each list, by bisection.
-__global__ void __launch_bounds__(kRowThreads) beam_merge_kernel(const BeamParams p) {
+// FP64 order as an unsigned key (no NaN; -0 as +0); every value's is above 0
+__device__ __forceinline__ uint64_t score_key(double s) {
+  const long long w = __double_as_longlong(s + 0.0);
+  return w < 0 ? ~(uint64_t)w : (uint64_t)w | 0x8000000000000000ull;
+}
+
+// The largest key of a warp; 64 bits by two 32-bit reductions.
+__device__ __forceinline__ uint64_t warp_max(uint64_t k) {
+  const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(k >> 32));
+  const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
+  return (uint64_t)hi << 32 | lo;
+}
+
+constexpr int kMergeThreads = 512;
+
+// One CTA per sequence.  A warp per beam joins the lists of its parts (a lane per part, n_out
+// rounds of a maximum over their heads), then one warp joins the beams' lists the same way
+// (two beams a lane) by score, ties to the lower beam.
+__global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamParams p, int parts) {
+  extern __shared__ uint64_t sm[];
   const int b = blockIdx.x, K = p.n_beams, take = min(p.n_out, p.vocab);
-  const unsigned char* rows = static_cast<const unsigned char*>(p.workspace) + (int64_t)b * K * beam_row_bytes(p.n_out);
-  for (int c = threadIdx.x; c < K * take; c += kRowThreads) {
-    const int i = c / take, e = c % take;
-    const unsigned char* mine = rows + i * beam_row_bytes(p.n_out);
-    const uint64_t k = reinterpret_cast<const uint64_t*>(mine + 8)[e];
-    const double s = reinterpret_cast<const BeamRow*>(mine)->offset + (double)beam_value((uint32_t)(k >> 32));
-    int rank = e;
-    for (int o = 0; o < K; ++o) {
-      if (o == i) continue;
-      const unsigned char* other = rows + o * beam_row_bytes(p.n_out);
-      const double off = reinterpret_cast<const BeamRow*>(other)->offset;
-      int lo = 0, hi = take;
-      while (lo < hi) {
-        const int mid = (lo + hi) / 2;
-        const double so = off + (double)beam_value((uint32_t)(reinterpret_cast<const uint64_t*>(other + 8)[mid] >> 32));
-        const bool better = so > s || (so == s && o < i);
-        if (better) lo = mid + 1;
-        else hi = mid;
+  double* offset = reinterpret_cast<double*>(sm);  // [K]: cum - logsumexp
+  uint64_t* lists = sm + K;                        // [K][take]
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t pb = beam_part_bytes(p.n_out);
+  const unsigned char* first = static_cast<const unsigned char*>(p.workspace) + (int64_t)b * K * parts * pb;
+  griddep_wait();
+  if (tid < K) {
+    const float cum = p.cum[(int64_t)b * K + tid];
+    const unsigned char* w = first + (int64_t)tid * parts * pb;
+    float top = -INFINITY;
+    for (int s = 0; s < parts; ++s) top = fmaxf(top, reinterpret_cast<const BeamPart*>(w + s * pb)->top);
+    double off = cum > -INFINITY ? (double)fminf(cum, 3.402823466e38f) : 0.0;
+    if (top > -INFINITY) {  // (a dead or finished beam has no top)
+      double sum = 0.0;
+      for (int s = 0; s < parts; ++s) {
+        const BeamPart* q = reinterpret_cast<const BeamPart*>(w + s * pb);
+        sum += q->sum * exp((double)q->top - (double)top);
       }
-      rank += lo;
+      off -= (double)top + log(sum);
     }
-    if (rank < p.n_out) {
-      const int64_t at = (int64_t)b * p.n_out + rank;
+    offset[tid] = off;
+  }
+  if (parts == 1) {
+    for (int e = tid; e < K * take; e += kMergeThreads)
+      lists[e] = reinterpret_cast<const uint64_t*>(first + e / take * pb + sizeof(BeamPart))[e % take];
+  } else {
+    for (int i = warp; i < K; i += kMergeThreads / 32) {
+      const uint64_t* mine = reinterpret_cast<const uint64_t*>(first + ((int64_t)i * parts + min(lane, parts - 1)) * pb +
+                                                               sizeof(BeamPart));
+      int at = 0;
+      uint64_t k = lane < parts ? mine[0] : 0ull;
+      uint64_t next = lane < parts && take > 1 ? mine[1] : 0ull;
+      for (int r = 0; r < take; ++r) {
+        const uint64_t m = warp_max(k);
+        if (lane == 0) lists[i * take + r] = m;
+        if (k == m && m) {
+          ++at;
+          k = next;
+          next = at + 1 < take ? mine[at + 1] : 0ull;
+        }
+      }
+    }
+  }
+  __syncthreads();
+  if (warp != 0) return;
+  int at[2] = {0, 0};
+  uint64_t score[2];
+  auto load = [&](int e) {
+    const int i = lane + 32 * e;
+    const uint64_t k = i < K && at[e] < take ? lists[i * take + at[e]] : 0ull;
+    score[e] = k ? score_key(offset[i] + (double)beam_value((uint32_t)(k >> 32))) : 0ull;
+  };
+  load(0);
+  load(1);
+  for (int r = 0; r < p.n_out; ++r) {
+    const int e = score[1] > score[0];
+    const uint64_t m = warp_max(score[e]);
+    const uint32_t beam = __reduce_min_sync(0xffffffffu, score[0] == m ? lane : score[1] == m ? lane + 32 : 255);
+    if ((beam & 31) == lane) {
+      const int i = (int)beam, w = i >> 5;
+      const uint64_t k = lists[i * take + (w ? at[1] : at[0])];
+      const int64_t to = (int64_t)b * p.n_out + r;
       const int token = (int)(0xffffffffu - (uint32_t)k);
-      p.parent[at] = i;
-      p.token[at] = token;
-      p.score[at] = (float)s;
-      if (p.finished_out) p.finished_out[at] = (p.finished && p.finished[b * K + i] != 0) || token == p.eos;
+      p.parent[to] = i;
+      p.token[to] = token;
+      p.score[to] = (float)(offset[i] + (double)beam_value((uint32_t)(k >> 32)));
+      if (p.finished_out) p.finished_out[to] = (p.finished && p.finished[(int64_t)b * K + i] != 0) || token == p.eos;
+      if (w) {
+        ++at[1];
+        load(1);
+      } else {
+        ++at[0];
+        load(0);
+      }
     }
   }
 }
@@ -120,15 +365,18 @@ __global__ void __launch_bounds__(kRowThreads) beam_merge_kernel(const BeamParam
 }  // namespace
 
 size_t beam_workspace_bytes(int64_t n_seqs, int64_t n_beams, int64_t vocab, int64_t n_out) {
-  return (size_t)(n_seqs * n_beams * beam_row_bytes((int)n_out));
+  const int64_t rows = n_seqs * n_beams;
+  return rows ? (size_t)(rows * beam_parts(rows, vocab) * beam_part_bytes((int)n_out)) : 0;
 }
 
 cudaError_t launch_beam_select(const BeamParams& p, cudaStream_t stream) {
-  const int rows = p.n_seqs * p.n_beams;
-  if (p.io == LA_F32) beam_row_kernel<float><<<rows, kRowThreads, 0, stream>>>(p);
-  else beam_row_kernel<__nv_bfloat16><<<rows, kRowThreads, 0, stream>>>(p);
-  beam_merge_kernel<<<p.n_seqs, kRowThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  const int rows = p.n_seqs * p.n_beams, parts = beam_parts(rows, p.vocab);
+  if (p.io == LA_F32) beam_row_kernel<float><<<rows * parts, kRowThreads, 0, stream>>>(p, parts);
+  else beam_row_kernel<__nv_bfloat16><<<rows * parts, kRowThreads, 0, stream>>>(p, parts);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const int take = p.n_out < p.vocab ? p.n_out : p.vocab;
+  return launch_dependent(beam_merge_kernel, p.n_seqs, kMergeThreads, 8 * p.n_beams * (1 + take), stream, p, parts);
 }
 
 }  // namespace la

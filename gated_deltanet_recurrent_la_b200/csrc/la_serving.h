@@ -101,6 +101,7 @@ struct SlabList {
   int32_t n;
   void* data[kMaxSlabs];
   int64_t bytes[kMaxSlabs];   // of one slot, a multiple of 16
+  int32_t first[kMaxSlabs + 1];  // pieces of a slot before slab l (the launcher's)
 };
 cudaError_t launch_pool_reorder(const SlabList& slabs, int32_t n_slots, int32_t n_seqs, int32_t n_beams,
                                 const int32_t* slots, const int32_t* parent, int32_t* new_slots, int32_t* err,
@@ -115,5 +116,23 @@ cudaError_t launch_pool_compact(const SlabList& slabs, int32_t n_slots, const in
                                 int32_t* remap, int32_t* moves, int32_t* counts, int32_t* err, cudaStream_t stream);
 cudaError_t launch_pool_remap(int64_t n, const int32_t* table, int32_t n_slots, const int32_t* remap,
                               int32_t* new_table, int32_t* err, cudaStream_t stream);
+
+// Launch that may start before the stream's previous kernel has drained (the kernel itself
+// waits for it with griddep_wait before it touches memory).
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*fn)(P...), int grid, int threads, int smem, cudaStream_t stream, const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, P(args)...);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
 
 }  // namespace la

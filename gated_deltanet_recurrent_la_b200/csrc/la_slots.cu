@@ -1,8 +1,9 @@
 // la_slots.cu -- slot bookkeeping on the device, over the slabs of all layers at once: beam
 // reordering, allocation by reference counts, forking, freeing, compaction.
 //
-// Each call is a small kernel that decides which slots move (whole numbers only, the same
-// answer whatever the order of the threads) and one copy kernel for the slabs of all layers.
+// Which slots move is decided by whole numbers, the same whatever the order of the threads: by a
+// kernel of one CTA (allocation, compaction) or by the copying warps themselves (reordering).
+// One copy kernel moves them in the slabs of all layers.
 // Sources and destinations of the copies of one call never meet, so they run in any order.
 #include <algorithm>
 
@@ -13,121 +14,184 @@ namespace la {
 
 namespace {
 
-constexpr int kCopyThreads = 256;
-constexpr int kCopyUnroll = 4;
-constexpr int64_t kCopyVecs = (int64_t)kCopyThreads * kCopyUnroll;  // 16 KiB
+// ---- copies ---------------------------------------------------------------------------------
+// Slots of many slabs, bound by HBM (each byte read and written once).  A slot is cut into
+// pieces of at most 8 KiB; every warp of a persistent grid takes pieces a grid apart (the pairs
+// that move are spread over all SMs whatever their number), its lanes work out 32 pieces at a
+// time (source, destination, bytes), and one lane moves them with bulk copies through a ring of
+// kStages buffers in shared memory: loads kLead ahead of the stores, no registers in between.
+constexpr int kCopyWarps = 6;
+constexpr int kStages = 4;
+constexpr int kLead = 2;
+constexpr int kPiece = 8192;
+constexpr int kCopySmem = kCopyWarps * kStages * kPiece + kCopyWarps * kStages * 8;
+
+enum PairKind { kPairsList, kPairsMoves, kPairsBeams };
 
 struct Pairs {
-  int32_t n;                 // upper bound
-  const int32_t* n_dev;      // nullptr, or the number on the device
-  const int32_t* src;        // slot of pair i: src[i], or src[group base + via[i]]
-  const int32_t* via;
-  int32_t group;
-  const int32_t* dst;        // dst[i], or dst[src[i]] with dst_by_src
-  int32_t dst_by_src;
+  int32_t kind;
+  int32_t n;                // pairs (list, beams), their upper bound (moves)
   int32_t n_slots;
-  int32_t chunks_per_slot;
+  // list: src[i] -> dst[i].  moves: src[i] -> dst[src[i]], i < *count.  beams: see beam_pair
+  const int32_t* src;
+  const int32_t* dst;
+  const int32_t* count;
+  int32_t n_beams;
+  const int32_t* parent;
+  int32_t* new_slots;
+  int32_t* err;
 };
 
-__global__ void __launch_bounds__(kCopyThreads) slab_copy_kernel(const SlabList slabs, const Pairs q) {
-  const int n = q.n_dev ? min(q.n, __ldg(q.n_dev)) : q.n;
-  const int64_t work = (int64_t)n * q.chunks_per_slot;
-  for (int64_t w = blockIdx.x; w < work; w += gridDim.x) {
-    const int i = (int)(w / q.chunks_per_slot);
-    int chunk = (int)(w % q.chunks_per_slot);
-    int s;
-    if (q.via) {
-      const int v = __ldg(q.via + i);
-      if (v < 0 || v >= q.group) continue;  // reported by the planning kernel
-      s = __ldg(q.src + i / q.group * q.group + v);
+// New beam i = (sequence, j) of a reordering: its slot, and the slot it is copied from (-1: it
+// stays where its parent was).  The first child of a beam keeps its slot, the k-th other child
+// takes the slot of the k-th beam without a child.  Whole numbers, the same in every warp.
+__device__ __forceinline__ int beam_pair(const Pairs& q, int i, int& from, uint32_t& bad) {
+  const int K = q.n_beams, j = i % K;
+  const int32_t* slots = q.src + (i - j);
+  const int32_t* par = q.parent + (i - j);
+  uint64_t has = 0, others = 0;  // beams with a child; new beams that are not a first child
+  bad = 0u;
+  for (int e = 0; e < K; ++e) {
+    const int s = __ldg(slots + e), pe = __ldg(par + e);
+    if (s < 0 || s >= q.n_slots) bad |= LA_DEVERR_READ_SLOT;
+    if (pe < 0 || pe >= K) {
+      bad |= LA_DEVERR_TREE;
     } else {
-      s = __ldg(q.src + i);
+      if (has >> pe & 1) others |= 1ull << e;
+      has |= 1ull << pe;
     }
-    if (s < 0 || s >= q.n_slots) continue;
-    const int d = __ldg(q.dst + (q.dst_by_src ? s : i));
-    if (d < 0 || d >= q.n_slots || d == s) continue;
-    int l = 0;
-    for (; l < slabs.n; ++l) {
-      const int c = (int)((slabs.bytes[l] / 16 + kCopyVecs - 1) / kCopyVecs);
-      if (chunk < c) break;
-      chunk -= c;
+  }
+  from = -1;
+  if (bad) return -1;  // this sequence stays as it is
+  const int mine = __ldg(par + j);
+  if (!(others >> j & 1)) return __ldg(slots + mine);
+  uint64_t spare = ~has;
+  for (int k = __popcll(others & ((1ull << j) - 1)); k > 0; --k) spare &= spare - 1;
+  from = __ldg(slots + mine);
+  return __ldg(slots + __ffsll((long long)spare) - 1);
+}
+
+__global__ void __launch_bounds__(kCopyWarps * 32) slab_copy_kernel(const SlabList slabs, const Pairs q) {
+  extern __shared__ __align__(128) unsigned char sm[];
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kCopyWarps * kStages * kPiece);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  unsigned char* ring = sm + warp * kStages * kPiece;
+  uint64_t* full = bars + warp * kStages;
+  if (lane == 0) {
+    for (int s = 0; s < kStages; ++s) mbar_init(full + s, 1);
+    mbar_init_fence();
+  }
+  __syncwarp();
+  griddep_wait();
+  const int n = q.kind == kPairsMoves ? min(q.n, __ldg(q.count)) : q.n;
+  const int per = slabs.first[slabs.n];
+  const int64_t work = (int64_t)n * per, step = (int64_t)gridDim.x * kCopyWarps;
+  uint32_t loaded = 0, stored = 0;  // lane 0: pieces so far
+  bool ok = true;
+  uint32_t bytes_of[kStages];       // of the pieces in the ring
+  unsigned char* to_of[kStages];
+  auto store = [&] {
+    const uint32_t s = stored % kStages;
+    ok = mbar_wait(full + s, (stored / kStages) & 1u);
+    if (!ok) return;
+    unsigned char* to = nullptr;
+    uint32_t nb = 0;
+#pragma unroll
+    for (int e = 0; e < kStages; ++e)
+      if (s == (uint32_t)e) {
+        to = to_of[e];
+        nb = bytes_of[e];
+      }
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(to), "r"(smem_addr(ring + s * kPiece)),
+                 "r"(nb)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    ++stored;
+  };
+  for (int64_t w0 = blockIdx.x + (int64_t)warp * gridDim.x; w0 < work; w0 += 32 * step) {
+    const int64_t w = w0 + lane * step;
+    const unsigned char* from = nullptr;
+    unsigned char* to = nullptr;
+    uint32_t bytes = 0;
+    if (w < work) {
+      const int i = (int)(w / per), piece = (int)(w % per);
+      int s, d;
+      if (q.kind == kPairsBeams) {
+        uint32_t bad;
+        d = beam_pair(q, i, s, bad);
+        if (piece == 0) {
+          q.new_slots[i] = d;
+          if (bad && i % q.n_beams == 0) report(q.err, bad);
+        }
+      } else {
+        s = __ldg(q.src + i);
+        d = s >= 0 && s < q.n_slots ? __ldg(q.dst + (q.kind == kPairsMoves ? s : i)) : -1;
+      }
+      if (s >= 0 && s < q.n_slots && d >= 0 && d < q.n_slots && d != s) {
+        int l = 0, hi = slabs.n - 1;
+        while (l < hi) {  // the slab of the piece
+          const int mid = (l + hi + 1) / 2;
+          if (slabs.first[mid] <= piece) l = mid;
+          else hi = mid - 1;
+        }
+        const int64_t size = slabs.bytes[l], off = (int64_t)(piece - slabs.first[l]) * kPiece;
+        from = static_cast<const unsigned char*>(slabs.data[l]) + s * size + off;
+        to = static_cast<unsigned char*>(slabs.data[l]) + d * size + off;
+        bytes = (uint32_t)(size - off < kPiece ? size - off : kPiece);
+      }
     }
-    const int64_t vecs = slabs.bytes[l] / 16;
-    const uint4* from = reinterpret_cast<const uint4*>(static_cast<unsigned char*>(slabs.data[l]) + s * slabs.bytes[l]);
-    uint4* to = reinterpret_cast<uint4*>(static_cast<unsigned char*>(slabs.data[l]) + d * slabs.bytes[l]);
-    const int64_t v0 = chunk * kCopyVecs + threadIdx.x;
-    uint4 x[kCopyUnroll];
+    for (uint32_t left = __ballot_sync(0xffffffffu, bytes != 0u); left; left &= left - 1) {
+      const int e = __ffs(left) - 1;
+      const uint64_t f = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(from), e);
+      const uint64_t t = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(to), e);
+      const uint32_t nb = __shfl_sync(0xffffffffu, bytes, e);
+      if (lane == 0 && ok) {
+        // the buffer's last store has been read out: at most kStages - 1 - kLead younger ones are not
+        asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kStages - 1 - kLead) : "memory");
+        const uint32_t s = loaded % kStages;
 #pragma unroll
-    for (int e = 0; e < kCopyUnroll; ++e)
-      if (v0 + e * kCopyThreads < vecs) x[e] = __ldcs(from + v0 + e * kCopyThreads);
-#pragma unroll
-    for (int e = 0; e < kCopyUnroll; ++e)
-      if (v0 + e * kCopyThreads < vecs) to[v0 + e * kCopyThreads] = x[e];
+        for (int c = 0; c < kStages; ++c)
+          if (s == (uint32_t)c) {
+            to_of[c] = reinterpret_cast<unsigned char*>(t);
+            bytes_of[c] = nb;
+          }
+        mbar_arrive_expect_tx(full + s, nb);
+        bulk_g2s(ring + s * kPiece, reinterpret_cast<const void*>(f), nb, full + s);
+        ++loaded;
+        if (loaded - stored > kLead) store();
+      }
+    }
+  }
+  if (lane == 0) {
+    while (ok && stored < loaded) store();
+    if (!ok) {
+      report(q.err, LA_DEVERR_TIMEOUT);
+      for (uint32_t e = stored + 1; e < loaded; ++e) mbar_wait(full + e % kStages, (e / kStages) & 1u);
+    }
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
 }
 
-int chunks_per_slot(const SlabList& slabs) {
-  int64_t c = 0;
-  for (int l = 0; l < slabs.n; ++l) c += (slabs.bytes[l] / 16 + kCopyVecs - 1) / kCopyVecs;
-  return (int)c;
-}
-
-cudaError_t copy_pairs(const SlabList& slabs, const Pairs& q, cudaStream_t stream) {
-  if (q.n == 0 || q.chunks_per_slot == 0) return cudaSuccess;
-  const int per_sm = prepare_kernel(reinterpret_cast<const void*>(&slab_copy_kernel), kCopyThreads, 0);
-  if (per_sm <= 0) return cudaErrorInvalidConfiguration;
-  const int64_t work = (int64_t)q.n * q.chunks_per_slot;
-  const int grid = (int)std::min<int64_t>(work, (int64_t)device_sm_count() * per_sm);
-  slab_copy_kernel<<<grid, kCopyThreads, 0, stream>>>(slabs, q);
-  return cudaGetLastError();
+cudaError_t copy_pairs(const SlabList& in, const Pairs& q, cudaStream_t stream) {
+  if (q.n == 0) return cudaSuccess;
+  SlabList slabs = in;
+  int64_t per = 0;
+  for (int l = 0; l < slabs.n; ++l) {
+    slabs.first[l] = (int32_t)per;
+    per += (slabs.bytes[l] + kPiece - 1) / kPiece;
+  }
+  if (per > INT32_MAX) return cudaErrorInvalidValue;
+  slabs.first[slabs.n] = (int32_t)per;
+  if (prepare_kernel(reinterpret_cast<const void*>(&slab_copy_kernel), kCopyWarps * 32, kCopySmem) <= 0)
+    return cudaErrorInvalidConfiguration;
+  const int grid = (int)std::min<int64_t>((int64_t)q.n * per, device_sm_count());
+  return launch_dependent(slab_copy_kernel, grid, kCopyWarps * 32, kCopySmem, stream, slabs, q);
 }
 
 // ---- planning ------------------------------------------------------------------------------
 
-// One CTA of 64 threads per sequence, thread j = new beam j: the first child of a beam keeps
-// its slot, the k-th other child takes the slot of the k-th beam without a child.
-__global__ void __launch_bounds__(64) reorder_plan_kernel(int K, int n_slots, const int32_t* slots, const int32_t* parent,
-                                                          int32_t* new_slots, int32_t* err) {
-  __shared__ int par[64];
-  __shared__ uint32_t has[2], other[2];
-  const int j = threadIdx.x;
-  const int64_t base = (int64_t)blockIdx.x * K;
-  bool bad = false;
-  int slot = 0;
-  if (j < K) {
-    par[j] = parent[base + j];
-    slot = slots[base + j];
-    bad = slot < 0 || slot >= n_slots;
-  }
-  if (j < 2) has[j] = 0u;
-  const bool bad_parent = j < K && (par[j] < 0 || par[j] >= K);
-  const bool any_slot = __syncthreads_or(bad), any_parent = __syncthreads_or(bad_parent);
-  if (any_slot || any_parent) {  // this sequence stays as it is
-    if (j == 0) report(err, (any_slot ? LA_DEVERR_READ_SLOT : 0u) | (any_parent ? LA_DEVERR_TREE : 0u));
-    if (j < K) new_slots[base + j] = -1;
-    return;
-  }
-  bool first = true;
-  if (j < K) {
-    for (int i = 0; i < j; ++i) first &= par[i] != par[j];
-    atomicOr(&has[par[j] >> 5], 1u << (par[j] & 31));
-  }
-  const uint32_t rest = __ballot_sync(0xffffffffu, j < K && !first);
-  if ((j & 31) == 0) other[j >> 5] = rest;
-  __syncthreads();
-  if (j >= K) return;
-  int from = par[j];
-  if (!first) {
-    int k = __popc(other[j >> 5] & ((1u << (j & 31)) - 1u)) + (j >= 32 ? __popc(other[0]) : 0);
-    for (from = 0; from < K; ++from) {  // the k-th beam without a child
-      if (has[from >> 5] >> (from & 31) & 1u) continue;
-      if (k-- == 0) break;
-    }
-  }
-  new_slots[base + j] = slots[base + from];
-}
-
 constexpr int kPlanThreads = 1024;
+static_assert(kPlanThreads == 32 * 32, "block_rank reads one count per lane");
 
 // Exclusive rank of `flag` among the CTA's threads in order, and the total.
 __device__ __forceinline__ int block_rank(bool flag, int* warp_count, int& total) {
@@ -136,12 +200,9 @@ __device__ __forceinline__ int block_rank(bool flag, int* warp_count, int& total
   __syncthreads();
   if (lane == 0) warp_count[warp] = __popc(m);
   __syncthreads();
-  int before = 0;
-  total = 0;
-  for (int w = 0; w < kPlanThreads / 32; ++w) {
-    before += w < warp ? warp_count[w] : 0;
-    total += warp_count[w];
-  }
+  const int c = warp_count[lane];
+  total = __reduce_add_sync(0xffffffffu, c);
+  const int before = __reduce_add_sync(0xffffffffu, lane < warp ? c : 0);
   return before + __popc(m & ((1u << lane) - 1u));
 }
 
@@ -287,15 +348,15 @@ __global__ void __launch_bounds__(256) remap_kernel(int64_t n, const int32_t* ta
 cudaError_t launch_pool_reorder(const SlabList& slabs, int32_t n_slots, int32_t n_seqs, int32_t n_beams,
                                 const int32_t* slots, const int32_t* parent, int32_t* new_slots, int32_t* err,
                                 cudaStream_t stream) {
-  reorder_plan_kernel<<<n_seqs, 64, 0, stream>>>(n_beams, n_slots, slots, parent, new_slots, err);
   Pairs q{};
+  q.kind = kPairsBeams;
   q.n = n_seqs * n_beams;
-  q.src = slots;
-  q.via = parent;
-  q.group = n_beams;
-  q.dst = new_slots;
   q.n_slots = n_slots;
-  q.chunks_per_slot = chunks_per_slot(slabs);
+  q.src = slots;
+  q.n_beams = n_beams;
+  q.parent = parent;
+  q.new_slots = new_slots;
+  q.err = err;
   return copy_pairs(slabs, q, stream);
 }
 
@@ -314,26 +375,31 @@ cudaError_t launch_pool_ref(int32_t* ref, int32_t n_slots, int32_t n, const int3
 cudaError_t launch_pool_fork(const SlabList& slabs, int32_t* ref, int32_t n_slots, int32_t n, const int32_t* src_slots,
                              int32_t* new_slots, int32_t* err, cudaStream_t stream) {
   alloc_kernel<<<1, kPlanThreads, 0, stream>>>(ref, n_slots, n, new_slots, src_slots, err);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
   Pairs q{};
+  q.kind = kPairsList;
   q.n = n;
+  q.n_slots = n_slots;
   q.src = src_slots;
   q.dst = new_slots;
-  q.n_slots = n_slots;
-  q.chunks_per_slot = chunks_per_slot(slabs);
+  q.err = err;
   return copy_pairs(slabs, q, stream);
 }
 
 cudaError_t launch_pool_compact(const SlabList& slabs, int32_t n_slots, const int32_t* ref, int32_t* new_ref,
                                 int32_t* remap, int32_t* moves, int32_t* counts, int32_t* err, cudaStream_t stream) {
   compact_plan_kernel<<<1, kPlanThreads, 0, stream>>>(n_slots, ref, new_ref, remap, moves, counts);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
   Pairs q{};
+  q.kind = kPairsMoves;
   q.n = n_slots / 2;  // at most as many moves as free places
-  q.n_dev = counts + 1;
+  q.n_slots = n_slots;
   q.src = moves;
   q.dst = remap;
-  q.dst_by_src = 1;
-  q.n_slots = n_slots;
-  q.chunks_per_slot = chunks_per_slot(slabs);
+  q.count = counts + 1;
+  q.err = err;
   return copy_pairs(slabs, q, stream);
 }
 

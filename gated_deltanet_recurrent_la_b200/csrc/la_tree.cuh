@@ -78,6 +78,28 @@ __device__ __forceinline__ int tree_span(const int32_t* cu, int total, int max_n
 }
 __device__ __forceinline__ uint32_t span_error(int n) { return n == -1 ? LA_DEVERR_CU_SEQLENS : LA_DEVERR_TREE; }
 
+// E consecutive state values, piece c of row i (columns E c ..), in FP32; E = 8, or 4 for FP32 states
+template <int E, typename ST, int DV>
+__device__ __forceinline__ void state_piece(const TileReader<ST>& S, int i, int c, float* x) {
+  if constexpr (std::is_same<ST, q8_t>::value) {
+    constexpr int NG = DV / 32;
+    const int e = S.row_info[i], idx = e >> 1;
+    if (e & 1) {
+      StateVec<__nv_bfloat16>::unpack(
+          __ldcs(reinterpret_cast<const uint4*>(S.tile + S.n8 * DV + S.n8 * NG * 4 + (idx * DV + 8 * c) * 2)), x);
+    } else {
+      const uint2 w = __ldcs(reinterpret_cast<const uint2*>(S.tile + idx * DV + 8 * c));
+      const uint32_t words[2] = {w.x, w.y};
+      q8_unpack<8>(words, reinterpret_cast<const float*>(S.tile + S.n8 * DV)[idx * NG + (c >> 2)], x);
+    }
+  } else {
+    constexpr int V = StateVec<ST>::kElems;
+    const uint4* p = reinterpret_cast<const uint4*>(S.tile + i * DV + E * c);
+#pragma unroll
+    for (int e = 0; e < E / V; ++e) StateVec<ST>::unpack(__ldcs(p + e), x + e * V);
+  }
+}
+
 // ---- verification ------------------------------------------------------------------------
 
 constexpr int kTreeThreads = 128;
@@ -263,120 +285,197 @@ cudaError_t launch_tree(const TreeParams& p, cudaStream_t stream) {
 
 // ---- commit ------------------------------------------------------------------------------------
 // S <- Gamma_leaf S0 + sum over the path's nodes s of (D_leaf,s k_s) u_s^T, rounded once at the
-// store.  One CTA per (sequence, state head), one column of d_v per thread.
+// store.  Bound by the state's bytes (read and written once): one CTA per (sequence, state
+// head) reads its whole tile into registers before it looks at the path, so that the loads
+// cover the dependent reads of leaf, parents, k and u; a thread's pieces lie in one column
+// group, so a path node costs it one piece of u and one factor per row.
+
+constexpr int kCommitThreads = 256;
+
+// Eight (q8, BF16) or four (FP32) consecutive values of a row.
+template <typename ST>
+struct CommitVec {
+  static constexpr int kElems = std::is_same<ST, float>::value ? 4 : 8;
+};
 
 template <int DK, int DV>
 __host__ __device__ constexpr int commit_smem(int rows) {
-  return 4 * (rows * (DK + DV) + DK + 2 * DK + rows);
+  return 4 * (rows * (DK + DV) + DK + 2 * DK + 4 * rows + 4);
 }
 
 template <typename ST, typename IT, int DK, int DV, bool KDA>
-__global__ void __launch_bounds__(DV < 32 ? 32 : DV) commit_kernel(const TreeCommitParams p, int rows) {
+__global__ void __launch_bounds__(kCommitThreads, 2) commit_kernel(const TreeCommitParams p, int rows) {
+  constexpr bool Q8 = std::is_same<ST, q8_t>::value;
+  constexpr int E = CommitVec<ST>::kElems, PR = DV / E;            // pieces of a row
+  constexpr int NP = DK * PR;
+  constexpr int ACT = NP < kCommitThreads ? NP : kCommitThreads;   // threads that hold pieces
+  constexpr int NPT = NP / ACT, RS = ACT / PR;                     // pieces of a thread, rows between them
   extern __shared__ __align__(16) float sm[];
   float* kc = sm;                 // [path][DK]: D_leaf,s k_s
   float* us = kc + rows * DK;     // [path][DV]
   float* G = us + rows * DV;      // [DK]
   int* src_info = reinterpret_cast<int*>(G + DK);  // [DK] (q8)
   int* dst_info = src_info + DK;
-  int* path = dst_info + DK;      // [rows]: leaf first
-  __shared__ int n_path;
+  int* par = dst_info + DK;       // [rows]
+  int* path = par + rows;         // [rows]: leaf first
+  float* gate = reinterpret_cast<float*>(path + rows);  // [rows]: of the path's nodes
+  float* dec = gate + rows;       // [rows]: D_leaf,s (scalar gates)
+  int* n_path = reinterpret_cast<int*>(dec + rows);
   const int H = p.n_v_heads;
   const int b = blockIdx.x / H, h = blockIdx.x % H;
   const int hq = h / (H / p.n_qk_heads);
-  const int tid = threadIdx.x, NT = blockDim.x;
+  const int tid = threadIdx.x;
+  const int rs = p.read_slot ? __ldg(p.read_slot + b) : b, ws = p.write_slot ? __ldg(p.write_slot + b) : b;
   int c0;
   const int n = tree_span(p.cu, p.total, p.max_nodes, b, c0);
+  const int leaf = __ldg(p.leaf + b);
   if (n < 0) {
     if (tid == 0) report(p.err, span_error(n));
     return;
   }
-  const int rs = p.read_slot ? __ldg(p.read_slot + b) : b, ws = p.write_slot ? __ldg(p.write_slot + b) : b;
   const bool r_ok = rs >= 0 && rs < p.src_slots, w_ok = ws >= 0 && ws < p.dst_slots;
   if (!r_ok || !w_ok) {
     if (tid == 0) report(p.err, (r_ok ? 0u : LA_DEVERR_READ_SLOT) | (w_ok ? 0u : LA_DEVERR_WRITE_SLOT));
     return;
   }
-  if (tid == 0) {
-    int m = 0, s = __ldg(p.leaf + b);
-    bool ok = s >= -1 && s < n;
-    while (ok && s >= 0) {
-      path[m++] = s;
-      const int up = __ldg(p.parent + c0 + s);
-      ok = up >= -1 && up < s;
-      s = up;
-    }
-    n_path = ok ? m : -1;
-  }
-  __syncthreads();
-  const int m = n_path;
-  if (m < 0) {
-    if (tid == 0) report(p.err, LA_DEVERR_TREE);
-    return;
-  }
-  constexpr bool Q8 = sizeof(ST) == sizeof(q8_t);
   if constexpr (Q8) {
     if (!q8_rows(p.src_mask + h * (DK / 32), DK, p.n_hp, src_info) ||
         !q8_rows(p.dst_mask + h * (DK / 32), DK, p.n_hp, dst_info)) {
       if (tid == 0) report(p.err, LA_DEVERR_Q8_MASK);
       return;
     }
+    __syncthreads();
+  }
+  const int row0 = tid / PR, col = tid % PR;
+  TileReader<ST> S;
+  S.init(p.src, (int64_t)rs * H + h, DK, DV, p.n_hp, src_info);
+  float x[NPT][E];
+  if (tid < ACT) {
+#pragma unroll
+    for (int k = 0; k < NPT; ++k) state_piece<E, ST, DV>(S, row0 + k * RS, col, x[k]);
+  }
+  for (int t = tid; t < n; t += kCommitThreads) par[t] = __ldg(p.parent + c0 + t);
+  __syncthreads();
+  if (tid == 0) {
+    int m = 0, s = leaf;
+    bool ok = s >= -1 && s < n;
+    while (ok && s >= 0) {
+      path[m++] = s;
+      const int up = par[s];
+      ok = up >= -1 && up < s;
+      s = up;
+    }
+    *n_path = ok ? m : -1;
+  }
+  __syncthreads();
+  const int m = *n_path;
+  if (m < 0) {
+    if (tid == 0) report(p.err, LA_DEVERR_TREE);
+    return;
+  }
+  if constexpr (Q8) {
     if (m == 0 && p.src_mask == p.dst_mask) {  // nothing accepted: the tile as it is
       const int64_t bytes = q8_tile_bytes(DK, DV, p.n_hp);
       const uint4* s = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(p.src) + ((int64_t)rs * H + h) * bytes);
       uint4* d = reinterpret_cast<uint4*>(static_cast<unsigned char*>(p.dst) + ((int64_t)ws * H + h) * bytes);
-      for (int i = tid; i < bytes / 16; i += NT) d[i] = s[i];
+      for (int i = tid; i < bytes / 16; i += kCommitThreads) d[i] = s[i];
       return;
     }
   }
   const IT* gk = static_cast<const IT*>(p.k);
-  for (int i = tid; i < DK; i += NT) {
-    float d = 1.0f;
-    for (int a = 0; a < m; ++a) {
-      const int64_t t = c0 + path[a];
-      kc[a * DK + i] = d * io_load(gk + (t * p.n_qk_heads + hq) * DK + i);
-      if (p.g) d *= KDA ? __ldg(p.g + (t * H + h) * DK + i) : __ldg(p.g + t * H + h);
+  if constexpr (KDA) {
+    for (int i = tid; i < DK; i += kCommitThreads) {
+      float d = 1.0f;
+#pragma unroll 4
+      for (int a = 0; a < m; ++a) {
+        const int64_t t = c0 + path[a];
+        kc[a * DK + i] = d * io_load(gk + (t * p.n_qk_heads + hq) * DK + i);
+        d *= __ldg(p.g + (t * H + h) * DK + i);
+      }
+      G[i] = d;
     }
-    G[i] = d;
+  } else if (m > 0) {
+    if (p.g) {
+      for (int a = tid; a < m; a += kCommitThreads) gate[a] = __ldg(p.g + (int64_t)(c0 + path[a]) * H + h);
+      __syncthreads();
+      for (int a = tid; a <= m; a += kCommitThreads) {
+        float d = 1.0f;
+        for (int e = 0; e < a; ++e) d *= gate[e];
+        if (a < m) dec[a] = d;
+        else G[0] = d;
+      }
+      __syncthreads();
+    }
+    for (int e = tid; e < m * DK; e += kCommitThreads) {
+      const int a = e / DK;
+      const float k = io_load(gk + ((int64_t)(c0 + path[a]) * p.n_qk_heads + hq) * DK + e % DK);
+      kc[e] = p.g ? dec[a] * k : k;
+    }
   }
-  for (int e = tid; e < m * DV; e += NT)
-    us[e] = __ldg(p.u + ((int64_t)(c0 + path[e / DV]) * H + h) * DV + e % DV);
+  for (int e = tid; e < m * (DV / 4); e += kCommitThreads)
+    *reinterpret_cast<float4*>(us + 4 * e) = __ldg(reinterpret_cast<const float4*>(
+        p.u + ((int64_t)(c0 + path[e / (DV / 4)]) * H + h) * DV + e % (DV / 4) * 4));
   __syncthreads();
-  TileReader<ST> S;
-  S.init(p.src, (int64_t)rs * H + h, DK, DV, p.n_hp, src_info);
-  const int j = tid;
-  if (j >= DV) return;
-  for (int i = 0; i < DK; ++i) {
-    float x = S.template at<DV>(i, j);
-    if (m > 0) x *= G[i];
-    for (int a = 0; a < m; ++a) x = fmaf(kc[a * DK + i], us[a * DV + j], x);
-    if constexpr (Q8) {
-      constexpr int NG = DV / 32;
-      const int n8 = DK - p.n_hp, e = dst_info[i], idx = e >> 1;
-      unsigned char* tile = static_cast<unsigned char*>(p.dst) + ((int64_t)ws * H + h) * q8_tile_bytes(DK, DV, p.n_hp);
-      float amax = fabsf(x);
+  if (tid >= ACT) return;
+  if (m > 0 && (KDA || p.g)) {
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+    for (int k = 0; k < NPT; ++k) {
+      const float g = G[KDA ? row0 + k * RS : 0];
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[k][e] *= g;
+    }
+  }
+  for (int a = 0; a < m; ++a) {
+    float y[E];
+#pragma unroll
+    for (int e = 0; e < E; e += 4) {
+      const float4 w = *reinterpret_cast<const float4*>(us + a * DV + col * E + e);
+      y[e] = w.x; y[e + 1] = w.y; y[e + 2] = w.z; y[e + 3] = w.w;
+    }
+#pragma unroll
+    for (int k = 0; k < NPT; ++k) {
+      const float f = kc[a * DK + row0 + k * RS];
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[k][e] = fmaf(f, y[e], x[k][e]);
+    }
+  }
+  if constexpr (Q8) {
+    constexpr int NG = DV / 32;
+    const int n8 = DK - p.n_hp;
+    unsigned char* tile = static_cast<unsigned char*>(p.dst) + ((int64_t)ws * H + h) * q8_tile_bytes(DK, DV, p.n_hp);
+#pragma unroll
+    for (int k = 0; k < NPT; ++k) {
+      const int e = dst_info[row0 + k * RS], idx = e >> 1;
+      float amax = 0.0f;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) amax = fmaxf(amax, fabsf(x[k][c]));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));  // 32 columns: four threads
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
       if (e & 1) {
-        reinterpret_cast<__nv_bfloat16*>(tile + n8 * DV + n8 * NG * 4)[idx * DV + j] = __float2bfloat16_rn(x);
+        reinterpret_cast<uint4*>(tile + n8 * DV + n8 * NG * 4)[idx * PR + col] = StateVec<__nv_bfloat16>::pack(x[k]);
       } else {
         float s, inv;
         q8_scales(amax, s, inv);
-        reinterpret_cast<int8_t*>(tile)[idx * DV + j] = (int8_t)(int)q8_code(x, inv);
-        if ((j & 31) == 0) reinterpret_cast<float*>(tile + n8 * DV)[idx * NG + (j >> 5)] = s;
+        uint32_t words[2];
+        q8_pack<8>(x[k], inv, words);
+        reinterpret_cast<uint2*>(tile)[idx * PR + col] = make_uint2(words[0], words[1]);
+        if ((col & 3) == 0) reinterpret_cast<float*>(tile + n8 * DV)[idx * NG + (col >> 2)] = s;
       }
-    } else {
-      io_store(static_cast<ST*>(p.dst) + ((int64_t)ws * H + h) * DK * DV + i * DV + j, x);
     }
+  } else {
+    uint4* tile = reinterpret_cast<uint4*>(static_cast<ST*>(p.dst) + ((int64_t)ws * H + h) * DK * DV);
+#pragma unroll
+    for (int k = 0; k < NPT; ++k) __stcs(tile + (row0 + k * RS) * PR + col, StateVec<ST>::pack(x[k]));
   }
 }
 
 template <typename ST, typename IT, int DK, int DV, bool KDA>
 cudaError_t launch_commit(const TreeCommitParams& p, cudaStream_t stream) {
   auto fn = &commit_kernel<ST, IT, DK, DV, KDA>;
-  constexpr int kThreads = DV < 32 ? 32 : DV;
-  if (prepare_kernel(reinterpret_cast<const void*>(fn), kThreads, commit_smem<DK, DV>(kMaxNodes)) <= 0)
+  if (prepare_kernel(reinterpret_cast<const void*>(fn), kCommitThreads, commit_smem<DK, DV>(kMaxNodes)) <= 0)
     return cudaErrorInvalidConfiguration;
-  fn<<<p.n_seqs * p.n_v_heads, kThreads, commit_smem<DK, DV>(p.max_nodes), stream>>>(p, p.max_nodes);
+  const int rows = (p.max_nodes + 3) / 4 * 4;
+  fn<<<p.n_seqs * p.n_v_heads, kCommitThreads, commit_smem<DK, DV>(rows), stream>>>(p, rows);
   return cudaGetLastError();
 }
 

@@ -92,27 +92,6 @@ __device__ __forceinline__ void store_terms(unsigned char* dst, int stride, cons
   }
 }
 
-// eight consecutive state values (columns 8 c .. of row i) in FP32
-template <typename ST, int DV>
-__device__ __forceinline__ void state_piece(const TileReader<ST>& S, int i, int c, float* x) {
-  if constexpr (std::is_same<ST, q8_t>::value) {
-    constexpr int NG = DV / 32;
-    const int e = S.row_info[i], idx = e >> 1;
-    if (e & 1) {
-      StateVec<__nv_bfloat16>::unpack(
-          __ldg(reinterpret_cast<const uint4*>(S.tile + S.n8 * DV + S.n8 * NG * 4 + (idx * DV + 8 * c) * 2)), x);
-    } else {
-      const uint2 w = __ldg(reinterpret_cast<const uint2*>(S.tile + idx * DV + 8 * c));
-      const uint32_t words[2] = {w.x, w.y};
-      q8_unpack<8>(words, __ldg(reinterpret_cast<const float*>(S.tile + S.n8 * DV) + idx * NG + (c >> 2)), x);
-    }
-  } else {
-    const uint4* p = reinterpret_cast<const uint4*>(S.tile + i * DV + 8 * c);
-    StateVec<float>::unpack(__ldg(p), x);
-    StateVec<float>::unpack(__ldg(p + 1), x + 4);
-  }
-}
-
 template <int VEC>
 __device__ __forceinline__ void lds_vec(const float* p, float* x) {
   if constexpr (VEC == 4) {
@@ -377,7 +356,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) tree_tc_kernel(const TreeParams
 #pragma unroll
       for (int e = 0; e < kPieces; ++e) {
         const int at = tid + e * kTcThreads;
-        state_piece<ST, DV>(S, st * C::kRows + at / (DV / 8), at % (DV / 8), x[e]);
+        state_piece<8, ST, DV>(S, st * C::kRows + at / (DV / 8), at % (DV / 8), x[e]);
       }
       if (st > 0) done();  // the stage's buffer is free
 #pragma unroll
