@@ -646,6 +646,7 @@ la_status la_state_tree(la_rule rule, const la_pool* src, const int32_t* read_sl
   if (st != LA_OK) return st;
   const la_shape& s = src->shape;
   if ((st = check_nodes(n_seqs, total_nodes, max_nodes, s.n_v_heads)) != LA_OK) return st;
+  if ((int64_t)s.n_v_heads * s.d_v * LA_TREE_MAX_NODES > UINT32_MAX) return LA_ERR_SHAPE;  // a tree's rows: 32-bit offsets
   if (!elem_bytes(io) || !la_shape_supported(s.d_k, s.d_v)) return LA_ERR_UNSUPPORTED;
   if (n_seqs == 0) return LA_OK;
   if (!cu_nodes) return LA_ERR_NULL;

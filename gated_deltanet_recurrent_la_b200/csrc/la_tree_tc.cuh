@@ -4,26 +4,34 @@
 // With K, Q the nodes' rows (n <= 64) and S0 the sequence's state, the dense parts of
 //   u_t = b_t (v_t - [S0^T (Gamma_t k_t) + sum_{s above t} (k_t . D_ts k_s) u_s])
 //   o_t = scale (S0^T (Gamma_t q_t) + sum_{s above or at t} (q_t . D_ts k_s) u_s)
-// are two products of the stacked rows A = [K; Q] (2 R of the M = 128 rows, R = n rounded up to
-// 16):  A K^T  [128 x R], whose entries on a node's path, times D_ts, are the pair coefficients,
-// and A S0  [128 x d_v].  Rows and columns of absent nodes hold what shared memory held: an MMA
-// row depends on its own row of A only, and off-path coefficients are never read, so nothing
-// of them (nor a non-finite value of another branch) reaches a result.
+// are two products with the stacked rows A = [K; Q] (2 R rows, R = n rounded up to 16):
+//   A K^T     [128 x R], a node per tensor-memory lane: the pair coefficients, of which a lane
+//             keeps those on its node's path, times D_ts, packed along the path;
+//   S0^T A^T  [128 x 2 R], a column of d_v per lane.
+// Rows and columns of absent nodes hold what shared memory held: they reach only results that
+// nothing reads, and off-path coefficients are dropped, so a non-finite value of another branch
+// reaches nothing either.
 //
 // Precision: the accumulators are FP32.  BF16 operands are multiplied exactly; an FP32 operand
 // (FP32 q and k, an FP32 or q8 state, the kda rows scaled by Gamma) is cut into three BF16
 // terms of 8 significand bits each, exact together, and the products of terms i + j <= 2 are
 // summed: what is left out is below 2^-23 of the product.
 //
-// The substitution along the paths stays in FP32 on the CUDA cores, eight nodes at a time: a
-// warp per node adds the nodes above of earlier blocks, then one thread per column solves the
-// block in registers, then a warp per node adds the block's own part to the output.  It takes
-// 2 (path length) d_v FMAs a node whatever the tree; only ancestors are touched.
+// The substitution along the paths is FP32 on the CUDA cores with one thread per column of d_v:
+// it takes S0^T k_t and S0^T q_t from its own tensor-memory lane and keeps its column of V, then
+// U, in shared memory (over the operands), so the nodes follow one another without a barrier;
+// only ancestors are touched, two FMAs for each.  Two nodes at a time: a warp's instructions
+// come about 5 cycles apart when each waits for the one before.  Paths are padded to fours with
+// entries that point to a row of zeros, so the loop has no predicates, and it is kept rolled:
+// unrolled over eight nodes it ran out of the instruction caches (570 cycles a node).
 //
-// One CTA of 8 warps per (sequence, state head); the MMA results live in 128 tensor-memory
-// columns (the pair product first, the state product over it once it is read) and then go to
-// shared memory over the operands, so four CTAs fit an SM for small trees, two at 64 nodes.
+// One CTA of 4 warps per (sequence, state head), 8 where operands are cut into terms (the cutting
+// and the kda decays use them).  Bound by latency within a CTA (loads, MMA, path), which the
+// other CTAs of the SM cover: four fit for trees of up to 32 nodes; above that a BF16 state comes
+// in two halves of its rows, so that three fit.
 #pragma once
+
+#include <utility>
 
 #include "la_tree.cuh"
 #include "la_umma.cuh"
@@ -31,35 +39,40 @@
 namespace la {
 namespace tree {
 
-constexpr int kTcThreads = 256;
-constexpr uint32_t kTcCols = 128;
-
 template <typename ST, typename IT, int DK, int DV, bool KDA>
 struct TcCfg {
   static constexpr int TA = (KDA || sizeof(IT) == 4) ? 3 : 1;       // BF16 terms of A
   static constexpr int TS = std::is_same<ST, __nv_bfloat16>::value ? 1 : 3;  // and of S0
-  static constexpr int PA = DK / 64, PV = DV / 64;                  // panels of 64 columns
-  static constexpr int kRows = TS == 1 ? DK : 64;                   // rows of S0 staged at a time
-  static constexpr int kStagesS = DK / kRows;
-  static constexpr int kXs = DV + 4;                                // padded row of X (floats)
+  static constexpr int kThreads = TA == 1 && TS == 1 ? 128 : 256;
+  static constexpr int kMinCtas = kThreads == 128 ? 4 : 2;          // 128 registers a thread
+  static constexpr int PA = DK / 64;                                // panels of 64 columns
+  __host__ __device__ static constexpr int rows_s(int R) { return TS == 1 && R <= 32 ? DK : 64; }  // of S0, at a time
+  __host__ __device__ static constexpr int panel_s(int R) { return rows_s(R) * 128; }
+  __host__ __device__ static constexpr int term_s(int R) { return DV / 64 * panel_s(R); }
   __host__ __device__ static constexpr int panel_a(int R) { return 2 * R * 128; }
   __host__ __device__ static constexpr int bytes_a(int R) { return TA * PA * panel_a(R); }
-  static constexpr int kTermS = PV * kRows * 128;
-  static constexpr int kBytesS = TS * kTermS;
-  // operands, under them the results X [2 R][kXs]; an MMA reads 128 rows from any panel of A
+  // operands; over them U [R][DV] and a row of zeros.  A K^T reads 128 rows from any panel of A, S0^T A^T two panels
+  // of 64 columns from any term of S0.
   __host__ __device__ static constexpr int region(int R) {
-    int x = bytes_a(R) + kBytesS;
+    int x = bytes_a(R) + (TS - 1) * term_s(R) + 2 * panel_s(R);
     if (KDA && bytes_a(R) + R * DK * 8 > x) x = bytes_a(R) + R * DK * 8;  // K and g in FP32
-    if (2 * R * kXs * 4 > x) x = 2 * R * kXs * 4;
+    if ((R + 1) * DV * 4 > x) x = (R + 1) * DV * 4;
     if (bytes_a(R) - panel_a(R) + 16384 > x) x = bytes_a(R) - panel_a(R) + 16384;
     return (x + 15) / 16 * 16;
   }
-  __host__ __device__ static constexpr int cs(int R) { return R + 4; }  // padded row of the coefficients
-  // + coefficients KK, QK [R][R + 4], path lists [R][R] bytes, 6 arrays of R words, q8 rows, misc
-  __host__ __device__ static constexpr int smem(int R) {
-    return 1024 + region(R) + 2 * R * (R + 4) * 4 + R * R + 6 * R * 4 + DK * 4 + 32;
-  }
+  // paths: entries (at most t for node t, rounded up to fours, four for node 0) as two
+  // coefficients and a place (the count is a multiple of 8)
+  __host__ __device__ static constexpr int entries(int R) { return R * (R + 2) / 2 + 8; }
+  static constexpr int smem(int R) { return 1024 + region(R) + entries(R) * 9 + R * 64 + R * 8 + DK * 4 + 32; }
+  // tensor memory: S0^T A^T [2 R], before it A K^T [R]
+  __host__ __device__ static constexpr uint32_t cols(int R) { return R <= 16 ? 32 : R <= 32 ? 64 : 128; }
 };
+// entries kept for node t, and the first of them
+__device__ __forceinline__ int path_size(int t) { return max(4, (t + 3) & ~3); }
+__device__ __forceinline__ int path_at(int t) {
+  const int a = (t + 3) >> 2;  // of the nodes 1 .. t - 1, four each have 1, 2, .. fours
+  return t == 0 ? 0 : 4 + 8 * a * (a - 1) + 4 * a * (t - 4 * a + 3);
+}
 
 // x = hi + mid + lo, each a BF16 (by truncation, exact while nothing underflows; a non-finite x
 // gives non-finite terms)
@@ -92,44 +105,63 @@ __device__ __forceinline__ void store_terms(unsigned char* dst, int stride, cons
   }
 }
 
-template <int VEC>
-__device__ __forceinline__ void lds_vec(const float* p, float* x) {
-  if constexpr (VEC == 4) {
-    const float4 v = *reinterpret_cast<const float4*>(p);
-    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-  } else {
-    const float2 v = *reinterpret_cast<const float2*>(p);
-    x[0] = v.x; x[1] = v.y;
-  }
+// What the solve reads of a node: one record, so that its loads need one address.
+struct NodeRecord {
+  float gamma, b, self;   // product of the path's gates, write strength, q . k
+  int path;               // length | (number of the first four entries) << 16
+  uint32_t at[4];         // the nearest four: byte offset of their row of U,
+  float2 coef[4];         // and their coefficients for u and o
+};
+
+// two columns of this thread's tensor-memory lane (wait_ld before they are used)
+__device__ __forceinline__ void tmem_ld2(uint32_t taddr, uint32_t& a, uint32_t& b) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(taddr) : "memory");
+}
+
+// if (bits & 1 << E): the next entry down, its coefficient x and place.  Predicated: as branches
+// the 64 columns of a row took 4 times as long.
+template <int E>
+__device__ __forceinline__ void take_entry(uint32_t bits, uint32_t& coef, uint32_t& place, float x, int s) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b32 t;\n\t"
+      "and.b32 t, %2, %5;\n\tsetp.ne.u32 p, t, 0;\n\t"
+      "@p add.s32 %0, %0, -8;\n\t@p add.s32 %1, %1, -1;\n\t"
+      "@p st.shared.f32 [%0], %3;\n\t@p st.shared.u8 [%1], %4;\n\t}"
+      : "+r"(coef), "+r"(place)
+      : "r"(bits), "f"(x), "r"(s), "n"(1 << E)
+      : "memory");
+}
+template <int... E>
+__device__ __forceinline__ void take_entries(uint32_t bits, uint32_t& coef, uint32_t& place, const uint32_t* w, int s,
+                                             std::integer_sequence<int, E...>) {
+  (take_entry<E>(bits, coef, place, __uint_as_float(w[E]), s + E), ...);
 }
 
 template <typename ST, typename IT, int DK, int DV, bool KDA>
-__global__ void __launch_bounds__(kTcThreads, 2) tree_tc_kernel(const TreeParams p, int R) {
+__global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg<ST, IT, DK, DV, KDA>::kMinCtas))
+    tree_tc_kernel(const TreeParams p, int R) {
   using C = TcCfg<ST, IT, DK, DV, KDA>;
-  constexpr int TA = C::TA, TS = C::TS, PA = C::PA;
+  constexpr int TA = C::TA, TS = C::TS, PA = C::PA, NT = C::kThreads;
   extern __shared__ __align__(16) unsigned char raw[];
   unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-  const int bytesA = C::bytes_a(R), panelA = C::panel_a(R), cs = C::cs(R);
+  const int bytesA = C::bytes_a(R), panelA = C::panel_a(R);
   unsigned char* smA = sm;
   unsigned char* smS = sm + bytesA;
-  float* X = reinterpret_cast<float*>(sm);                       // [2 R][kXs], after the products
-  float* KK = reinterpret_cast<float*>(sm + C::region(R));       // [R][cs]
-  float* QK = KK + R * cs;
-  unsigned char* list = reinterpret_cast<unsigned char*>(QK + R * cs);  // [R][R]: nodes above, of earlier blocks
-  float* gate = reinterpret_cast<float*>(list + R * R);          // [R]
-  float* gamma = gate + R;
-  float* bta = gamma + R;
-  int* par = reinterpret_cast<int*>(bta + R);
-  int* len = par + R;                                            // entries of the node's list
-  int* own = len + R;                                            // nodes above in its own block, a bit each
-  int* row_info = own + R;                                       // [DK] (q8)
-  uint64_t* bar = reinterpret_cast<uint64_t*>(row_info + DK);
-  uint32_t* tm = reinterpret_cast<uint32_t*>(bar + 1);
+  float* U = reinterpret_cast<float*>(sm);                           // [R][DV], after the products
+  float* coef = reinterpret_cast<float*>(sm + C::region(R));         // entries: (of u, of o), nearest node first
+  NodeRecord* node = reinterpret_cast<NodeRecord*>(coef + 2 * C::entries(R));  // [R]
+  unsigned char* place = reinterpret_cast<unsigned char*>(node + R);  // entries: the node above
+  float* gate = reinterpret_cast<float*>(place + C::entries(R));     // [R]
+  int* par = reinterpret_cast<int*>(gate + R);                       // [R]
+  int* row_info = par + R;                                           // [DK] (q8)
+  uint64_t* bar = reinterpret_cast<uint64_t*>(row_info + DK);        // A K^T, S0^T A^T
+  uint32_t* tm = reinterpret_cast<uint32_t*>(bar + 2);
 
   const int H = p.n_v_heads;
   const int b = blockIdx.x / H, h = blockIdx.x % H;
   const int hq = h / (H / p.n_qk_heads);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int slot = p.read_slot ? __ldg(p.read_slot + b) : b;
   int c0;
   const int n = tree_span(p.cu, p.total, p.max_nodes, b, c0);
   if (n < 0) {
@@ -137,81 +169,94 @@ __global__ void __launch_bounds__(kTcThreads, 2) tree_tc_kernel(const TreeParams
     return;
   }
   if (n == 0) return;
-  const int slot = p.read_slot ? __ldg(p.read_slot + b) : b;
   if (slot < 0 || slot >= p.src_slots) {
     if (tid == 0) report(p.err, LA_DEVERR_READ_SLOT);
     return;
   }
-  bool bad = false;
-  for (int t = tid; t < n; t += kTcThreads) {
-    const int pt = __ldg(p.parent + c0 + t);
-    bad |= pt < -1 || pt >= t;
-    par[t] = pt;
-    gate[t] = !KDA && p.g ? __ldg(p.g + (int64_t)(c0 + t) * H + h) : 1.0f;
-    bta[t] = p.use_beta ? __ldg(p.beta + (int64_t)(c0 + t) * H + h) : 1.0f;
+  int my_par = -1;
+  float my_gate = 1.0f, my_beta = 1.0f;
+  if (tid < n) {
+    my_par = __ldg(p.parent + c0 + tid);
+    if (!KDA && p.g) my_gate = __ldg(p.g + (int64_t)(c0 + tid) * H + h);
+    if (p.use_beta) my_beta = __ldg(p.beta + (int64_t)(c0 + tid) * H + h);
   }
   // BF16 operands straight to shared memory: the rows of K and Q first, the state behind them
   const IT* gk = static_cast<const IT*>(p.k);
   const IT* gq = static_cast<const IT*>(p.q);
   const int64_t row0 = ((int64_t)c0 * p.n_qk_heads + hq) * DK, row_step = (int64_t)p.n_qk_heads * DK;
   if constexpr (TA == 1) {
-    for (int e = tid; e < 2 * n * (DK / 8); e += kTcThreads) {
-      const int r = e / (DK / 8), ch = e % (DK / 8), t = r < n ? r : r - n;
-      cp_async_16(smA + umma::panel_piece(2 * R, r < n ? t : R + t, ch), (r < n ? gk : gq) + row0 + t * row_step + ch * 8);
+    // (a thread's rows lie a multiple of 8 apart: the swizzle is the same in all of them)
+    constexpr int RS = NT / (DK / 8);
+    const int t0 = tid / (DK / 8), ch = tid % (DK / 8);
+    unsigned char* dst = smA + umma::panel_piece(2 * R, t0, ch);
+    const IT* fk = gk + row0 + t0 * row_step + ch * 8;
+    const IT* fq = gq + row0 + t0 * row_step + ch * 8;
+    for (int t = t0; t < n; t += RS, dst += RS * 128, fk += RS * row_step, fq += RS * row_step) {
+      cp_async_16(dst, fk);
+      cp_async_16(dst + R * 128, fq);
     }
     cp_async_commit();
   }
   TileReader<ST> S;
   S.init(p.src, (int64_t)slot * H + h, DK, DV, p.src_n_hp, row_info);
-  if constexpr (TS == 1 && !KDA) {
-    for (int e = tid; e < DK * (DV / 8); e += kTcThreads)
-      cp_async_16(smS + umma::panel_piece(C::kRows, e / (DV / 8), e % (DV / 8)), S.tile + e * 8);
-    cp_async_commit();
-  }
+  const int rows = C::rows_s(R), panelS = C::panel_s(R), termS = C::term_s(R), stages = DK / rows;
+  auto state_async = [&](int st) {
+    if constexpr (TS == 1) {
+      constexpr int RS = NT / (DV / 8);
+      unsigned char* dst = smS + umma::panel_piece(rows, tid / (DV / 8), tid % (DV / 8));
+      const ST* src = S.tile + st * rows * DV + tid * 8;
+#pragma unroll 8
+      for (int i = 0; i < rows / RS; ++i) cp_async_16(dst + i * RS * 128, src + i * RS * DV);
+      cp_async_commit();
+    }
+  };
+  if constexpr (!KDA) state_async(0);
   bool mask_ok = true;
   if constexpr (std::is_same<ST, q8_t>::value) mask_ok = q8_rows(p.src_mask + h * (DK / 32), DK, p.src_n_hp, row_info);
-  if (__syncthreads_or(bad) || !mask_ok) {
+  if (tid < n) {
+    par[tid] = my_par;
+    gate[tid] = my_gate;
+    node[tid].gamma = 1.0f;
+    node[tid].b = my_beta;
+  }
+  if (__syncthreads_or(tid < n && (my_par < -1 || my_par >= tid)) || !mask_ok) {
     cp_async_wait<0>();
     if (tid == 0) report(p.err, !mask_ok ? LA_DEVERR_Q8_MASK : LA_DEVERR_TREE);
     return;
   }
-  if (warp == 7) umma::alloc(tm, kTcCols);
+  if (warp == NT / 32 - 1) umma::alloc(tm, C::cols(R));
   if (tid == 0) {
     mbar_init(bar, 1);
+    mbar_init(bar + 1, 1);
     mbar_init_fence();
   }
-  // v of a warp's node is read a block ahead
-  constexpr int VEC = DV / 32;
-  const IT* gv = static_cast<const IT*>(p.v);
-  auto value_at = [&](int t) { return ((int64_t)(c0 + t) * H + h) * DV + lane * VEC; };
-  float vnext[VEC];
-  if (warp < n) load_f32<IT, VEC>(gv + value_at(warp), vnext);
+  if (TS == 1 && stages > 1 && tid == 0)  // the second half on its way to L2
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(S.tile + rows * DV), "r"((DK - rows) * DV * 2));
 
-  // lists of the nodes above, and the decays on the way to them
-  if (tid < 2 * R) {
-    const int t = tid < R ? tid : tid - R;
-    if (t < n) {
-      float* D = (tid < R ? KK : QK) + t * cs;
-      int m = 0, bits = 0;
-      float d = 1.0f;
-      const int t0 = t & ~7;
-      for (int s = t; s >= 0; s = par[s]) {
-        if constexpr (!KDA) {
-          D[s] = d;
-          d *= gate[s];
-        }
-        if (tid < R && s != t) {
-          if (s >= t0) bits |= 1 << (s - t0);
-          else list[t * R + m++] = (unsigned char)s;
-        }
-      }
-      if (tid < R) {
-        len[t] = m;
-        own[t] = bits;
-        gamma[t] = d;
-      }
+  // the nodes above; thread t for the coefficients of u, R + t for those of o
+  uint64_t above = 0;
+  const bool is_q = tid >= R;
+  const int t_own = is_q ? tid - R : tid;
+  const bool own = !KDA && tid < 2 * R && t_own < n;
+  if (own)
+    for (int s = par[t_own]; s >= 0; s = par[s]) above |= 1ull << s;
+  // The end of node t's path of m entries: up to the next four, entries of factor 0 and the row
+  // of zeros; then its record's length and offsets.  Also for the node behind an odd last one.
+  auto finish = [&](int t, int m) {
+    const int first = path_at(t);
+    for (int i = m; i < max(4, (m + 3) & ~3); ++i) {
+      reinterpret_cast<float2*>(coef)[first + i] = make_float2(0.0f, 0.0f);
+      place[first + i] = (unsigned char)R;
     }
-  }
+    node[t].path = m | first << 14;
+    const uint32_t four = *reinterpret_cast<const uint32_t*>(place + first);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      node[t].at[e] = (four >> (8 * e) & 255) * (DV * 4);
+      if (e >= m) node[t].coef[e] = make_float2(0.0f, 0.0f);
+    }
+  };
+  if (tid == 0 && (n & 1)) finish(n, 0);
 
   if constexpr (KDA) {
     // K and g in FP32 behind A; a warp per node walks its path with one decay per channel, forms
@@ -219,24 +264,32 @@ __global__ void __launch_bounds__(kTcThreads, 2) tree_tc_kernel(const TreeParams
     constexpr int CH = DK / 32;
     float* Kf = reinterpret_cast<float*>(smS);
     float* Gf = Kf + R * DK;
-    for (int e = tid; e < n * (DK / 4); e += kTcThreads) {
+    for (int e = tid; e < n * (DK / 4); e += NT) {
       const int t = e / (DK / 4), c = e % (DK / 4) * 4;
       load_f32<IT, 4>(gk + row0 + t * row_step + c, Kf + t * DK + c);
       *reinterpret_cast<float4*>(Gf + t * DK + c) =
           __ldg(reinterpret_cast<const float4*>(p.g + ((int64_t)(c0 + t) * H + h) * DK + c));
     }
     __syncthreads();
-    for (int t = warp; t < n; t += kTcThreads / 32) {
+    for (int t = warp; t < n; t += NT / 32) {
       float kt[CH], qt[CH], d[CH];
       load_f32<IT, CH>(gq + row0 + t * row_step + lane * CH, qt);
+      float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         kt[c] = Kf[t * DK + lane * CH + c];
-        d[c] = 1.0f;
+        d[c] = Gf[t * DK + lane * CH + c];
+        v[0] = fmaf(qt[c], kt[c], v[0]);
       }
-      for (int s = t; s >= 0;) {  // two nodes of the path at a time: their reductions overlap
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
+      if (lane == 0) node[t].self = v[0];
+      float2* at = reinterpret_cast<float2*>(coef) + path_at(t);
+      int m = 0;
+      for (int s = par[t]; s >= 0;) {  // two nodes of the path at a time: their reductions overlap
         const int s2 = par[s];
-        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = 0.0f;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
           const float x = d[c] * Kf[s * DK + lane * CH + c];
@@ -258,15 +311,21 @@ __global__ void __launch_bounds__(kTcThreads, 2) tree_tc_kernel(const TreeParams
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[e] += __shfl_xor_sync(0xffffffffu, v[e], off);
         if (lane == 0) {
-          KK[t * cs + s] = v[0];
-          QK[t * cs + s] = v[1];
+          at[m] = make_float2(v[0], v[1]);
+          place[path_at(t) + m] = (unsigned char)s;
           if (s2 >= 0) {
-            KK[t * cs + s2] = v[2];
-            QK[t * cs + s2] = v[3];
+            at[m + 1] = make_float2(v[2], v[3]);
+            place[path_at(t) + m + 1] = (unsigned char)s2;
+          }
+          if (m < 4) {
+            node[t].coef[m] = make_float2(v[0], v[1]);
+            node[t].coef[m + 1] = make_float2(v[2], v[3]);
           }
         }
+        m += s2 >= 0 ? 2 : 1;
         s = s2 >= 0 ? par[s2] : -1;
       }
+      if (lane == 0) finish(t, m);
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         kt[c] *= d[c];
@@ -275,14 +334,10 @@ __global__ void __launch_bounds__(kTcThreads, 2) tree_tc_kernel(const TreeParams
       store_terms<CH>(smA + umma::panel_off(2 * R, t, lane * CH), PA * panelA, kt);
       store_terms<CH>(smA + umma::panel_off(2 * R, R + t, lane * CH), PA * panelA, qt);
     }
-    if constexpr (TS == 1) {  // the state goes over K and g
-      __syncthreads();
-      for (int e = tid; e < DK * (DV / 8); e += kTcThreads)
-        cp_async_16(smS + umma::panel_piece(C::kRows, e / (DV / 8), e % (DV / 8)), S.tile + e * 8);
-      cp_async_commit();
-    }
+    __syncthreads();  // the state goes over K and g
+    state_async(0);
   } else if constexpr (TA == 3) {
-    for (int e = tid; e < 2 * n * (DK / 8); e += kTcThreads) {
+    for (int e = tid; e < 2 * n * (DK / 8); e += NT) {
       const int r = e / (DK / 8), ch = e % (DK / 8), t = r < n ? r : r - n;
       float x[8];
       load_f32<IT, 8>((r < n ? gk : gq) + row0 + t * row_step + ch * 8, x);
@@ -297,17 +352,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) tree_tc_kernel(const TreeParams
   umma::fence_after();
   const uint32_t tmem = *tm;
   const uint64_t dA = umma::sdesc(smem_addr(smA), 16, 1024);
-  const uint64_t dS = umma::sdesc(smem_addr(smS), C::kRows * 128, 1024);
+  const uint64_t dS = umma::sdesc(smem_addr(smS), panelS, 1024);
   bool ok = true;
-  uint32_t phase = 0;
-  auto done = [&] {  // every MMA issued so far
-    ok &= mbar_wait(bar, phase & 1u);
-    ++phase;
-    umma::fence_after();
-  };
-  const uint32_t quarter = umma::taddr(tmem, (warp & 3) * 32, 0);
-  const int row = (warp & 3) * 32 + lane;
-  const bool mine = (warp & 3) * 32 < 2 * R;  // the warp's lanes hold rows of A
 
   if constexpr (!KDA) {
     if (tid == 0) {
@@ -325,167 +371,217 @@ __global__ void __launch_bounds__(kTcThreads, 2) tree_tc_kernel(const TreeParams
           }
       umma::commit(bar);
     }
-    done();
-    if (mine)
-      for (int c = (warp >> 2) * 16; c < R; c += 32) {
+    ok &= mbar_wait(bar, 0);
+    umma::fence_after();
+    if (warp < 4 && warp * 32 < 2 * R) {
+      const int m = __popcll(above), first = path_at(t_own);
+      // nearest first: the places fall as s rises (both threads of a node write them, the same)
+      uint32_t at = smem_addr(coef + 2 * (first + m) + is_q), pl = smem_addr(place + first + m);
+#pragma unroll 1
+      for (int c = 0; c < R; c += 16) {
+        const uint32_t bits = own ? (uint32_t)(above >> c) & 0xffffu : 0u;
+        const bool diag = own && is_q && t_own >> 4 == c >> 4;
+        if (!__any_sync(0xffffffffu, bits || diag)) continue;
         uint32_t w[16];
-        umma::ld16(quarter + c, w);
+        umma::ld16(umma::taddr(tmem, warp * 32, c), w);
         umma::wait_ld();
-        if (row < 2 * R) {
-          float4* D = reinterpret_cast<float4*>((row < R ? KK + row * cs : QK + (row - R) * cs) + c);
+        take_entries(bits, at, pl, w, c, std::make_integer_sequence<int, 16>());
+        if (__any_sync(0xffffffffu, diag)) {
+          uint32_t self = 0;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float4 x = D[e];
-            x.x *= __uint_as_float(w[4 * e]);
-            x.y *= __uint_as_float(w[4 * e + 1]);
-            x.z *= __uint_as_float(w[4 * e + 2]);
-            x.w *= __uint_as_float(w[4 * e + 3]);
-            D[e] = x;
-          }
+          for (int e = 0; e < 16; ++e) self = (t_own & 15) == e ? w[e] : self;
+          if (diag) node[t_own].self = __uint_as_float(self);
         }
       }
+    }
+    umma::fence_before();
   }
-  // the state product, over the pair product's columns
-  uint32_t acc = 0;
-  for (int st = 0; st < C::kStagesS; ++st) {
+  // S0^T A^T, over the columns of A K^T
+  auto issue = [&](int st) {
+    umma::fence_after();
+    const uint32_t id = umma::idesc_bf16(128, 2 * R, true, false);
+#pragma unroll
+    for (int i = 0; i < TA; ++i)
+#pragma unroll
+      for (int j = 0; j < TS; ++j)
+        if (i + j <= 2)
+          for (int kk = 0; kk < rows / 16; ++kk) {
+            const int ka = st * (rows / 16) + kk;
+            umma::mma(tmem, umma::sdesc_add(dS, j * termS + kk * 2048),
+                      umma::sdesc_add(dA, (i * PA + (ka >> 2)) * panelA + (ka & 3) * 32), id, st | i | j | kk);
+          }
+    umma::commit(bar + 1);
+  };
+  for (int st = 0; st < stages; ++st) {
     if constexpr (TS == 1) {
-      cp_async_wait<0>();
+      if (st > 0) {  // the buffer is free
+        ok &= mbar_wait(bar + 1, (st - 1) & 1);
+        state_async(st);
+      }
     } else {
-      constexpr int kPieces = C::kRows * (DV / 8) / kTcThreads;
+      constexpr int kPieces = 64 * (DV / 8) / NT;
       float x[kPieces][8];
 #pragma unroll
       for (int e = 0; e < kPieces; ++e) {
-        const int at = tid + e * kTcThreads;
-        state_piece<8, ST, DV>(S, st * C::kRows + at / (DV / 8), at % (DV / 8), x[e]);
+        const int at = tid + e * NT;
+        state_piece<8, ST, DV>(S, st * 64 + at / (DV / 8), at % (DV / 8), x[e]);
       }
-      if (st > 0) done();  // the stage's buffer is free
+      if (st > 0) ok &= mbar_wait(bar + 1, (st - 1) & 1);
 #pragma unroll
       for (int e = 0; e < kPieces; ++e) {
-        const int at = tid + e * kTcThreads;
-        store_terms<8>(smS + umma::panel_piece(C::kRows, at / (DV / 8), at % (DV / 8)), C::kTermS, x[e]);
+        const int at = tid + e * NT;
+        store_terms<8>(smS + umma::panel_piece(64, at / (DV / 8), at % (DV / 8)), termS, x[e]);
       }
     }
-    umma::fence_smem();
-    umma::fence_before();
-    __syncthreads();
-    if (tid == 0) {
-      umma::fence_after();
-      constexpr uint32_t id = umma::idesc_bf16(128, DV, false, true);
-#pragma unroll
-      for (int i = 0; i < TA; ++i)
-#pragma unroll
-        for (int j = 0; j < TS; ++j)
-          if (i + j <= 2)
-#pragma unroll
-            for (int kk = 0; kk < C::kRows / 16; ++kk) {
-              const int ka = st * (C::kRows / 16) + kk;
-              umma::mma(tmem, umma::sdesc_add(dA, i * PA * panelA + (ka >> 2) * panelA + (ka & 3) * 32),
-                        umma::sdesc_add(dS, j * C::kTermS + kk * 2048), id, acc);
-              acc = 1;
-            }
-      umma::commit(bar);
-    }
-  }
-  done();
-  // the results over the operands; a scalar gate's Gamma is a factor of the row
-  if (mine)
-    for (int c = (warp >> 2) * 16; c < DV; c += 32) {
-      uint32_t w[16];
-      umma::ld16(quarter + c, w);
-      umma::wait_ld();
-      if (row < 2 * R) {
-        float G = 1.0f;
-        if (!KDA) G = gamma[row < R ? row : row - R];
-        float4* D = reinterpret_cast<float4*>(X + row * C::kXs + c);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          D[e] = make_float4(G * __uint_as_float(w[4 * e]), G * __uint_as_float(w[4 * e + 1]),
-                             G * __uint_as_float(w[4 * e + 2]), G * __uint_as_float(w[4 * e + 3]));
-      }
-    }
-  umma::fence_before();
-  const bool failed = __syncthreads_or(!ok);
-  if (warp == 7) {
-    umma::fence_after();
-    umma::dealloc(tmem, kTcCols);
-  }
-  if (failed) {
-    if (tid == 0) report(p.err, LA_DEVERR_TIMEOUT);
-    return;
-  }
-
-  for (int t0 = 0; t0 < n; t0 += 8) {
-    const int t = t0 + warp;
-    float out[VEC];
-    if (t < n) {
-      float pred[VEC];
-      lds_vec<VEC>(X + t * C::kXs + lane * VEC, pred);
-      lds_vec<VEC>(X + (R + t) * C::kXs + lane * VEC, out);
-      const float* KKr = KK + t * cs;
-      const float* QKr = QK + t * cs;
-      const int m = len[t];
+    if (st == stages - 1 && own) {  // the decays along the path, while the state is on its way
+      float d = gate[t_own];
+      const int m = __popcll(above), first = path_at(t_own);
       for (int i = 0; i < m; i += 4) {
-        const uint32_t four = *reinterpret_cast<const uint32_t*>(list + t * R + i);
+        const uint32_t four = *reinterpret_cast<const uint32_t*>(place + first + i);
+        float c[4], gs[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if (i + e < m) {
-            const int s = (four >> (8 * e)) & 255;
-            float x[VEC];
-            lds_vec<VEC>(X + s * C::kXs + lane * VEC, x);
-            const float kk = KKr[s], qk = QKr[s];
+            c[e] = coef[2 * (first + i + e) + is_q];
+            gs[e] = gate[four >> (8 * e) & 255];
+          }
 #pragma unroll
-            for (int c = 0; c < VEC; ++c) {
-              pred[c] = fmaf(kk, x[c], pred[c]);
-              out[c] = fmaf(qk, x[c], out[c]);
-            }
+        for (int e = 0; e < 4; ++e)
+          if (i + e < m) {
+            c[e] *= d;
+            d *= gs[e];
+            if (i == 0) reinterpret_cast<float*>(node[t_own].coef + e)[is_q] = c[e];
+            else coef[2 * (first + i + e) + is_q] = c[e];
           }
       }
-#pragma unroll
-      for (int c = 0; c < VEC; ++c) X[t * C::kXs + lane * VEC + c] = p.predicts ? vnext[c] - pred[c] : vnext[c];
+      if (!is_q) {
+        node[t_own].gamma = d;
+        finish(t_own, m);
+      }
     }
-    if (t + 8 < n) load_f32<IT, VEC>(gv + value_at(t + 8), vnext);
+    if constexpr (TS == 1) cp_async_wait<0>();
+    umma::fence_smem();
     __syncthreads();
-    if (p.predicts) {
-      if (tid < DV) {
-        float x[8];
+    if (tid == 0) issue(st);
+  }
+
+  // v, on its way while the products end: 16 bytes at a time, then in FP32 where U will be
+  constexpr int PV = DV * (int)sizeof(IT) / 16, VE = 16 / (int)sizeof(IT);  // pieces of a row, values of a piece
+  constexpr int VN = kMaxNodes * PV / NT;
+  const int64_t base_v = ((int64_t)c0 * H + h) * DV, step_v = (int64_t)H * DV;
+  uint4 vr[VN];
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          if (t0 + r < n) {
-            float y = X[(t0 + r) * C::kXs + tid];
-            const int bits = own[t0 + r];
-            const float4 a = *reinterpret_cast<const float4*>(KK + (t0 + r) * cs + t0);
-            const float4 z = *reinterpret_cast<const float4*>(KK + (t0 + r) * cs + t0 + 4);
-            const float coef[8] = {a.x, a.y, a.z, a.w, z.x, z.y, z.z, z.w};
+  for (int e = 0; e < VN; ++e) {
+    const int at = tid + e * NT;
+    if (at < n * PV)
+      vr[e] = __ldg(reinterpret_cast<const uint4*>(static_cast<const IT*>(p.v) + base_v + at / PV * step_v) + at % PV);
+  }
+  ok &= mbar_wait(bar + 1, (stages - 1) & 1);
+  umma::fence_after();
 #pragma unroll
-            for (int s = 0; s < r; ++s)
-              if (bits >> s & 1) y = fmaf(-coef[s], x[s], y);
-            x[r] = bta[t0 + r] * y;
-            X[(t0 + r) * C::kXs + tid] = x[r];
-          }
-        }
-      }
-      __syncthreads();
-    }
-    if (t < n) {
-      const float* QKr = QK + t * cs;
-      for (int bits = own[t]; bits; bits &= bits - 1) {
-        const int s = t0 + __ffs(bits) - 1;
-        float x[VEC];
-        lds_vec<VEC>(X + s * C::kXs + lane * VEC, x);
-        const float qk = QKr[s];
+  for (int e = 0; e < VN; ++e) {
+    const int at = tid + e * NT;
+    if (at < n * PV) {
+      float x[VE];
+      StateVec<IT>::unpack(vr[e], x);
 #pragma unroll
-        for (int c = 0; c < VEC; ++c) out[c] = fmaf(qk, x[c], out[c]);
-      }
-      float x[VEC];
-      lds_vec<VEC>(X + t * C::kXs + lane * VEC, x);
-      const float qk = QKr[t];
-#pragma unroll
-      for (int c = 0; c < VEC; ++c) out[c] = p.scale * fmaf(qk, x[c], out[c]);
-      const int64_t at = value_at(t);
-      store_f32<IT, VEC>(static_cast<IT*>(p.o) + at, out);
-      if (p.u) store_f32<float, VEC>(p.u + at, x);
+      for (int c = 0; c < VE; c += 4)
+        *reinterpret_cast<float4*>(U + at / PV * DV + at % PV * VE + c) = make_float4(x[c], x[c + 1], x[c + 2], x[c + 3]);
     }
   }
+  if (tid < DV) U[R * DV + tid] = 0.0f;
+  const bool failed = __syncthreads_or(!ok);
+
+  if (!failed && tid < DV) {
+    uint32_t mine_k = umma::taddr(tmem, warp * 32, 0), mine_q = mine_k + R;
+    const float4* entry = reinterpret_cast<const float4*>(coef);       // two entries each
+    const uint32_t* places = reinterpret_cast<const uint32_t*>(place);  // four
+    const unsigned char* rows_u = reinterpret_cast<const unsigned char*>(U + tid);
+    float* mine = U + tid;
+    IT* go = static_cast<IT*>(p.o) + base_v + tid;
+    float* gu = p.u + base_v + tid;
+    uint32_t off = 0;
+    const uint32_t step = (uint32_t)step_v;  // (the host has checked that 64 rows of all heads fit 32 bits)
+    const bool store_u = p.u != nullptr;
+    const NodeRecord* rec = node;
+    uint32_t k0, k1, q0, q1;
+    tmem_ld2(mine_k, k0, k1);
+    tmem_ld2(mine_q, q0, q1);
+    auto row = [&](uint32_t at) { return *reinterpret_cast<const float*>(rows_u + at); };
+    auto further = [&](int path, float& pred, float& out) {
+      const int m = path & 255;
+      const float4* en = entry + 2 * (path >> 16);
+      const uint32_t* pl = places + (path >> 16);
+#pragma unroll 1
+      for (int i = 4; i < m; i += 4) {
+        en += 2;
+        ++pl;
+        const float4 c0 = en[0], c1 = en[1];
+        const uint32_t s = *pl;
+        const float x0 = row((s & 255u) * (DV * 4)), x1 = row((s >> 8 & 255u) * (DV * 4));
+        const float x2 = row((s >> 16 & 255u) * (DV * 4)), x3 = row((s >> 24) * (DV * 4));
+        pred = fmaf(c0.x, x0, pred), out = fmaf(c0.y, x0, out);
+        pred = fmaf(c0.z, x1, pred), out = fmaf(c0.w, x1, out);
+        pred = fmaf(c1.x, x2, pred), out = fmaf(c1.y, x2, out);
+        pred = fmaf(c1.z, x3, pred), out = fmaf(c1.w, x3, out);
+      }
+    };
+    umma::wait_ld();
+#pragma unroll 1
+    for (int t = 0; t < n; t += 2) {
+      asm volatile("" : "+r"(k0), "+r"(k1), "+r"(q0), "+r"(q1));  // not before the wait
+      const float4 ia = reinterpret_cast<const float4*>(rec)[0], ib = reinterpret_cast<const float4*>(rec)[4];
+      const uint4 oa = reinterpret_cast<const uint4*>(rec)[1], ob = reinterpret_cast<const uint4*>(rec)[5];
+      const float4 a0 = reinterpret_cast<const float4*>(rec)[2], a1 = reinterpret_cast<const float4*>(rec)[3];
+      const float4 b0 = reinterpret_cast<const float4*>(rec)[6], b1 = reinterpret_cast<const float4*>(rec)[7];
+      const float va = mine[0], vb = mine[DV];
+      const float xa0 = row(oa.x), xa1 = row(oa.y), xa2 = row(oa.z), xa3 = row(oa.w);
+      const float xb0 = row(ob.x), xb1 = row(ob.y), xb2 = row(ob.z), xb3 = row(ob.w);
+      float preda = ia.x * __uint_as_float(k0), outa = ia.x * __uint_as_float(q0);
+      float predb = ib.x * __uint_as_float(k1), outb = ib.x * __uint_as_float(q1);
+      preda = fmaf(a0.x, xa0, preda), outa = fmaf(a0.y, xa0, outa);
+      predb = fmaf(b0.z, xb1, predb), outb = fmaf(b0.w, xb1, outb);
+      preda = fmaf(a0.z, xa1, preda), outa = fmaf(a0.w, xa1, outa);
+      predb = fmaf(b1.x, xb2, predb), outb = fmaf(b1.y, xb2, outb);
+      preda = fmaf(a1.x, xa2, preda), outa = fmaf(a1.y, xa2, outa);
+      predb = fmaf(b1.z, xb3, predb), outb = fmaf(b1.w, xb3, outb);
+      preda = fmaf(a1.z, xa3, preda), outa = fmaf(a1.w, xa3, outa);
+      const int pa = __float_as_int(ia.w), pb = __float_as_int(ib.w);
+      if ((pa & 255) > 4) further(pa, preda, outa);
+      if ((pb & 255) > 4) further(pb, predb, outb);
+      const float xa = p.predicts ? ia.y * (va - preda) : va;
+      // the second node may continue the first
+      const float xp = ob.x == (uint32_t)t * (DV * 4) ? xa : xb0;
+      predb = fmaf(b0.x, xp, predb), outb = fmaf(b0.y, xp, outb);
+      const float xb = p.predicts ? ib.y * (vb - predb) : vb;
+      mine_k += 2;
+      mine_q += 2;
+      if (t + 2 < n) {  // a pair ahead of its use
+        tmem_ld2(mine_k, k0, k1);
+        tmem_ld2(mine_q, q0, q1);
+      }
+      mine[0] = xa;
+      mine[DV] = xb;
+      const bool both = t + 1 < n;
+      io_store(go + off, p.scale * fmaf(ia.z, xa, outa));
+      if (both) io_store(go + off + step, p.scale * fmaf(ib.z, xb, outb));
+      if (store_u) {
+        gu[off] = xa;
+        if (both) gu[off + step] = xb;
+      }
+      off += 2 * step;
+      mine += 2 * DV;
+      rec += 2;
+      umma::wait_ld();
+    }
+  }
+  umma::fence_before();
+  __syncthreads();
+  if (warp == NT / 32 - 1) {
+    umma::fence_after();
+    umma::dealloc(tmem, C::cols(R));
+  }
+  if (failed && tid == 0) report(p.err, LA_DEVERR_TIMEOUT);
 }
 
 template <typename ST, typename IT, int DK, int DV, bool KDA>
@@ -494,9 +590,9 @@ cudaError_t launch_tree_tc(const TreeParams& p, cudaStream_t stream) {
   const int R = (p.max_nodes + 15) / 16 * 16;
   auto fn = &tree_tc_kernel<ST, IT, DK, DV, KDA>;
   static_assert(C::smem(kMaxNodes) <= 227 * 1024, "shared memory");
-  if (prepare_kernel(reinterpret_cast<const void*>(fn), kTcThreads, C::smem(kMaxNodes)) <= 0)
+  if (prepare_kernel(reinterpret_cast<const void*>(fn), C::kThreads, C::smem(kMaxNodes)) <= 0)
     return cudaErrorInvalidConfiguration;
-  fn<<<p.n_seqs * p.n_v_heads, kTcThreads, C::smem(R), stream>>>(p, R);
+  fn<<<p.n_seqs * p.n_v_heads, C::kThreads, C::smem(R), stream>>>(p, R);
   return cudaGetLastError();
 }
 
