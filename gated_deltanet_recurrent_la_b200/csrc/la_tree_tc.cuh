@@ -31,8 +31,6 @@
 // in two halves of its rows, so that three fit.
 #pragma once
 
-#include <utility>
-
 #include "la_tree.cuh"
 #include "la_umma.cuh"
 
@@ -105,10 +103,27 @@ __device__ __forceinline__ void store_terms(unsigned char* dst, int stride, cons
   }
 }
 
+// Waits for a phase of `bar` at most 2^16 times 20 us, without reading a timer (the thread sleeps
+// in the test itself).  False when it gave up.
+__device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity) {
+  for (uint32_t polls = 0; polls < 1u << 16; ++polls) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(20000u)
+        : "memory");
+    if (done) return true;
+  }
+  return false;
+}
+
 // What the solve reads of a node: one record, so that its loads need one address.
 struct NodeRecord {
   float gamma, b, self;   // product of the path's gates, write strength, q . k
-  int path;               // length | (number of the first four entries) << 16
+  int path;               // length | (number of the first four entries) << 16 | (more than four) << 31
   uint32_t at[4];         // the nearest four: byte offset of their row of U,
   float2 coef[4];         // and their coefficients for u and o
 };
@@ -118,23 +133,11 @@ __device__ __forceinline__ void tmem_ld2(uint32_t taddr, uint32_t& a, uint32_t& 
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(taddr) : "memory");
 }
 
-// if (bits & 1 << E): the next entry down, its coefficient x and place.  Predicated: as branches
+// if (bit): x at shared address `at`.  Predicated, with the addresses formed outside: as branches
 // the 64 columns of a row took 4 times as long.
-template <int E>
-__device__ __forceinline__ void take_entry(uint32_t bits, uint32_t& coef, uint32_t& place, float x, int s) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b32 t;\n\t"
-      "and.b32 t, %2, %5;\n\tsetp.ne.u32 p, t, 0;\n\t"
-      "@p add.s32 %0, %0, -8;\n\t@p add.s32 %1, %1, -1;\n\t"
-      "@p st.shared.f32 [%0], %3;\n\t@p st.shared.u8 [%1], %4;\n\t}"
-      : "+r"(coef), "+r"(place)
-      : "r"(bits), "f"(x), "r"(s), "n"(1 << E)
-      : "memory");
-}
-template <int... E>
-__device__ __forceinline__ void take_entries(uint32_t bits, uint32_t& coef, uint32_t& place, const uint32_t* w, int s,
-                                             std::integer_sequence<int, E...>) {
-  (take_entry<E>(bits, coef, place, __uint_as_float(w[E]), s + E), ...);
+__device__ __forceinline__ void store_if(uint32_t bit, uint32_t at, float x) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %0, 0;\n\t@p st.shared.f32 [%1], %2;\n\t}" ::"r"(bit), "r"(at), "f"(x)
+               : "memory");
 }
 
 template <typename ST, typename IT, int DK, int DV, bool KDA>
@@ -143,7 +146,8 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
   using C = TcCfg<ST, IT, DK, DV, KDA>;
   constexpr int TA = C::TA, TS = C::TS, PA = C::PA, NT = C::kThreads;
   extern __shared__ __align__(16) unsigned char raw[];
-  unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  // (an offset, not a rounded address: the compiler has to see that this is shared memory)
+  unsigned char* sm = raw + ((0u - smem_addr(raw)) & 1023u);
   const int bytesA = C::bytes_a(R), panelA = C::panel_a(R);
   unsigned char* smA = sm;
   unsigned char* smS = sm + bytesA;
@@ -232,6 +236,17 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
   }
   if (TS == 1 && stages > 1 && tid == 0)  // the second half on its way to L2
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(S.tile + rows * DV), "r"((DK - rows) * DV * 2));
+  // v waits in registers until the products are done with the operands
+  constexpr int PV = DV * (int)sizeof(IT) / 16, VE = 16 / (int)sizeof(IT);  // pieces of a row of v, values of a piece
+  constexpr int VN = kMaxNodes * PV / NT;
+  const int64_t base_v = ((int64_t)c0 * H + h) * DV, step_v = (int64_t)H * DV;
+  uint4 vr[VN];
+#pragma unroll
+  for (int e = 0; e < VN; ++e) {
+    const int at = tid + e * NT;
+    if (at < n * PV)
+      vr[e] = __ldg(reinterpret_cast<const uint4*>(static_cast<const IT*>(p.v) + base_v + at / PV * step_v) + at % PV);
+  }
 
   // the nodes above; thread t for the coefficients of u, R + t for those of o
   uint64_t above = 0;
@@ -248,7 +263,7 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
       reinterpret_cast<float2*>(coef)[first + i] = make_float2(0.0f, 0.0f);
       place[first + i] = (unsigned char)R;
     }
-    node[t].path = m | first << 14;
+    node[t].path = m | first << 14 | (m > 4 ? 1 << 31 : 0);
     const uint32_t four = *reinterpret_cast<const uint32_t*>(place + first);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -371,12 +386,11 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
           }
       umma::commit(bar);
     }
-    ok &= mbar_wait(bar, 0);
+    ok &= tree_wait(bar, 0);
     umma::fence_after();
     if (warp < 4 && warp * 32 < 2 * R) {
-      const int m = __popcll(above), first = path_at(t_own);
-      // nearest first: the places fall as s rises (both threads of a node write them, the same)
-      uint32_t at = smem_addr(coef + 2 * (first + m) + is_q), pl = smem_addr(place + first + m);
+      // nearest first: the places fall as s rises
+      uint32_t at = smem_addr(coef + 2 * (path_at(t_own) + __popcll(above)) + is_q);
 #pragma unroll 1
       for (int c = 0; c < R; c += 16) {
         const uint32_t bits = own ? (uint32_t)(above >> c) & 0xffffu : 0u;
@@ -385,7 +399,12 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
         uint32_t w[16];
         umma::ld16(umma::taddr(tmem, warp * 32, c), w);
         umma::wait_ld();
-        take_entries(bits, at, pl, w, c, std::make_integer_sequence<int, 16>());
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const uint32_t bit = bits >> e & 1u;
+          at -= 8 * bit;
+          store_if(bit, at, __uint_as_float(w[e]));
+        }
         if (__any_sync(0xffffffffu, diag)) {
           uint32_t self = 0;
 #pragma unroll
@@ -415,7 +434,7 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
   for (int st = 0; st < stages; ++st) {
     if constexpr (TS == 1) {
       if (st > 0) {  // the buffer is free
-        ok &= mbar_wait(bar + 1, (st - 1) & 1);
+        ok &= tree_wait(bar + 1, (st - 1) & 1);
         state_async(st);
       }
     } else {
@@ -426,7 +445,7 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
         const int at = tid + e * NT;
         state_piece<8, ST, DV>(S, st * 64 + at / (DV / 8), at % (DV / 8), x[e]);
       }
-      if (st > 0) ok &= mbar_wait(bar + 1, (st - 1) & 1);
+      if (st > 0) ok &= tree_wait(bar + 1, (st - 1) & 1);
 #pragma unroll
       for (int e = 0; e < kPieces; ++e) {
         const int at = tid + e * NT;
@@ -436,15 +455,17 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
     if (st == stages - 1 && own) {  // the decays along the path, while the state is on its way
       float d = gate[t_own];
       const int m = __popcll(above), first = path_at(t_own);
+      uint64_t left = above;
       for (int i = 0; i < m; i += 4) {
-        const uint32_t four = *reinterpret_cast<const uint32_t*>(place + first + i);
         float c[4], gs[4];
+        int s[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (i + e < m) {
-            c[e] = coef[2 * (first + i + e) + is_q];
-            gs[e] = gate[four >> (8 * e) & 255];
-          }
+        for (int e = 0; e < 4; ++e) {
+          s[e] = left ? 63 - __clzll((long long)left) : 0;
+          left &= ~(1ull << s[e]);
+          c[e] = coef[2 * (first + i + e) + is_q];
+          gs[e] = gate[s[e]];
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if (i + e < m) {
@@ -452,6 +473,7 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
             d *= gs[e];
             if (i == 0) reinterpret_cast<float*>(node[t_own].coef + e)[is_q] = c[e];
             else coef[2 * (first + i + e) + is_q] = c[e];
+            if (!is_q) place[first + i + e] = (unsigned char)s[e];
           }
       }
       if (!is_q) {
@@ -465,18 +487,8 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
     if (tid == 0) issue(st);
   }
 
-  // v, on its way while the products end: 16 bytes at a time, then in FP32 where U will be
-  constexpr int PV = DV * (int)sizeof(IT) / 16, VE = 16 / (int)sizeof(IT);  // pieces of a row, values of a piece
-  constexpr int VN = kMaxNodes * PV / NT;
-  const int64_t base_v = ((int64_t)c0 * H + h) * DV, step_v = (int64_t)H * DV;
-  uint4 vr[VN];
-#pragma unroll
-  for (int e = 0; e < VN; ++e) {
-    const int at = tid + e * NT;
-    if (at < n * PV)
-      vr[e] = __ldg(reinterpret_cast<const uint4*>(static_cast<const IT*>(p.v) + base_v + at / PV * step_v) + at % PV);
-  }
-  ok &= mbar_wait(bar + 1, (stages - 1) & 1);
+  // v in FP32 where U will be
+  ok &= tree_wait(bar + 1, (stages - 1) & 1);
   umma::fence_after();
 #pragma unroll
   for (int e = 0; e < VN; ++e) {
@@ -510,8 +522,8 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
     auto row = [&](uint32_t at) { return *reinterpret_cast<const float*>(rows_u + at); };
     auto further = [&](int path, float& pred, float& out) {
       const int m = path & 255;
-      const float4* en = entry + 2 * (path >> 16);
-      const uint32_t* pl = places + (path >> 16);
+      const float4* en = entry + 2 * (path >> 16 & 0x7fff);
+      const uint32_t* pl = places + (path >> 16 & 0x7fff);
 #pragma unroll 1
       for (int i = 4; i < m; i += 4) {
         en += 2;
@@ -547,8 +559,10 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
       predb = fmaf(b1.z, xb3, predb), outb = fmaf(b1.w, xb3, outb);
       preda = fmaf(a1.z, xa3, preda), outa = fmaf(a1.w, xa3, outa);
       const int pa = __float_as_int(ia.w), pb = __float_as_int(ib.w);
-      if ((pa & 255) > 4) further(pa, preda, outa);
-      if ((pb & 255) > 4) further(pb, predb, outb);
+      if ((pa | pb) < 0) {
+        further(pa, preda, outa);
+        further(pb, predb, outb);
+      }
       const float xa = p.predicts ? ia.y * (va - preda) : va;
       // the second node may continue the first
       const float xp = ob.x == (uint32_t)t * (DV * 4) ? xa : xb0;
@@ -562,12 +576,15 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
       }
       mine[0] = xa;
       mine[DV] = xb;
+      // (behind an odd last node: that node once more, instead of a branch)
       const bool both = t + 1 < n;
-      io_store(go + off, p.scale * fmaf(ia.z, xa, outa));
-      if (both) io_store(go + off + step, p.scale * fmaf(ib.z, xb, outb));
+      const float ya = p.scale * fmaf(ia.z, xa, outa), yb = both ? p.scale * fmaf(ib.z, xb, outb) : ya;
+      const uint32_t off_b = both ? off + step : off;
+      io_store(go + off, ya);
+      io_store(go + off_b, yb);
       if (store_u) {
         gu[off] = xa;
-        if (both) gu[off + step] = xb;
+        gu[off_b] = both ? xb : xa;
       }
       off += 2 * step;
       mine += 2 * DV;
