@@ -65,8 +65,8 @@ struct TcCfg {
   // tensor memory: S0^T A^T [2 R], before it A K^T [R]
   __host__ __device__ static constexpr uint32_t cols(int R) { return R <= 16 ? 32 : R <= 32 ? 64 : 128; }
 };
-// entries kept for node t, and the first of them
-__device__ __forceinline__ int path_size(int t) { return max(4, (t + 3) & ~3); }
+// m entries rounded up to fours, at least one four; the first entry kept for node t
+__device__ __forceinline__ int path_size(int m) { return max(4, (m + 3) & ~3); }
 __device__ __forceinline__ int path_at(int t) {
   const int a = (t + 3) >> 2;  // of the nodes 1 .. t - 1, four each have 1, 2, .. fours
   return t == 0 ? 0 : 4 + 8 * a * (a - 1) + 4 * a * (t - 4 * a + 3);
@@ -125,7 +125,7 @@ struct NodeRecord {
   float gamma, b, self;   // product of the path's gates, write strength, q . k
   int path;               // length | (number of the first four entries) << 16 | (more than four) << 31
   uint32_t at[4];         // the nearest four: byte offset of their row of U,
-  float2 coef[4];         // and their coefficients for u and o
+  float coef[2][4];       // and their coefficients for u and o
 };
 
 // two columns of this thread's tensor-memory lane (wait_ld before they are used)
@@ -152,8 +152,9 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
   unsigned char* smA = sm;
   unsigned char* smS = sm + bytesA;
   float* U = reinterpret_cast<float*>(sm);                           // [R][DV], after the products
-  float* coef = reinterpret_cast<float*>(sm + C::region(R));         // entries: (of u, of o), nearest node first
-  NodeRecord* node = reinterpret_cast<NodeRecord*>(coef + 2 * C::entries(R));  // [R]
+  const int plane = C::entries(R);
+  float* coef = reinterpret_cast<float*>(sm + C::region(R));         // [2][entries]: of u, of o; nearest node first
+  NodeRecord* node = reinterpret_cast<NodeRecord*>(coef + 2 * plane);  // [R]
   unsigned char* place = reinterpret_cast<unsigned char*>(node + R);  // entries: the node above
   float* gate = reinterpret_cast<float*>(place + C::entries(R));     // [R]
   int* par = reinterpret_cast<int*>(gate + R);                       // [R]
@@ -250,25 +251,40 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
 
   // the nodes above; thread t for the coefficients of u, R + t for those of o
   uint64_t above = 0;
+  uint32_t four = 0x01010101u * R;  // the nearest four, R where there are fewer
   const bool is_q = tid >= R;
   const int t_own = is_q ? tid - R : tid;
   const bool own = !KDA && tid < 2 * R && t_own < n;
-  if (own)
-    for (int s = par[t_own]; s >= 0; s = par[s]) above |= 1ull << s;
-  // The end of node t's path of m entries: up to the next four, entries of factor 0 and the row
-  // of zeros; then its record's length and offsets.  Also for the node behind an odd last one.
+  if (own) {
+    uint32_t* words = reinterpret_cast<uint32_t*>(place + path_at(t_own));
+    uint32_t word = 0x01010101u * R;
+    int i = 0;
+    for (int s = par[t_own]; s >= 0; s = par[s]) {
+      above |= 1ull << s;
+      word = word ^ (uint32_t)(R ^ s) << (8 * (i & 3));
+      if ((++i & 3) == 0) {
+        if (i == 4) four = word;
+        if (!is_q) *words++ = word;
+        word = 0x01010101u * R;
+      }
+    }
+    if (i < 4) four = word;
+    if (!is_q && ((i & 3) || i == 0)) *words = word;
+  }
+  // For the kda walk and the node behind an odd last one: entries up to the next four (factor 0,
+  // row of zeros), then the record's length and offsets.
   auto finish = [&](int t, int m) {
     const int first = path_at(t);
-    for (int i = m; i < max(4, (m + 3) & ~3); ++i) {
-      reinterpret_cast<float2*>(coef)[first + i] = make_float2(0.0f, 0.0f);
+    for (int i = m; i < path_size(m); ++i) {
+      coef[first + i] = coef[plane + first + i] = 0.0f;
       place[first + i] = (unsigned char)R;
     }
     node[t].path = m | first << 14 | (m > 4 ? 1 << 31 : 0);
-    const uint32_t four = *reinterpret_cast<const uint32_t*>(place + first);
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(place + first);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      node[t].at[e] = (four >> (8 * e) & 255) * (DV * 4);
-      if (e >= m) node[t].coef[e] = make_float2(0.0f, 0.0f);
+      node[t].at[e] = (w >> (8 * e) & 255) * (DV * 4);
+      if (e >= m) node[t].coef[0][e] = node[t].coef[1][e] = 0.0f;
     }
   };
   if (tid == 0 && (n & 1)) finish(n, 0);
@@ -299,7 +315,7 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
       if (lane == 0) node[t].self = v[0];
-      float2* at = reinterpret_cast<float2*>(coef) + path_at(t);
+      float* at = coef + path_at(t);
       int m = 0;
       for (int s = par[t]; s >= 0;) {  // two nodes of the path at a time: their reductions overlap
         const int s2 = par[s];
@@ -326,15 +342,19 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[e] += __shfl_xor_sync(0xffffffffu, v[e], off);
         if (lane == 0) {
-          at[m] = make_float2(v[0], v[1]);
+          at[m] = v[0];
+          at[plane + m] = v[1];
           place[path_at(t) + m] = (unsigned char)s;
           if (s2 >= 0) {
-            at[m + 1] = make_float2(v[2], v[3]);
+            at[m + 1] = v[2];
+            at[plane + m + 1] = v[3];
             place[path_at(t) + m + 1] = (unsigned char)s2;
           }
           if (m < 4) {
-            node[t].coef[m] = make_float2(v[0], v[1]);
-            node[t].coef[m + 1] = make_float2(v[2], v[3]);
+            node[t].coef[0][m] = v[0];
+            node[t].coef[1][m] = v[1];
+            node[t].coef[0][m + 1] = v[2];
+            node[t].coef[1][m + 1] = v[3];
           }
         }
         m += s2 >= 0 ? 2 : 1;
@@ -390,7 +410,7 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
     umma::fence_after();
     if (warp < 4 && warp * 32 < 2 * R) {
       // nearest first: the places fall as s rises
-      uint32_t at = smem_addr(coef + 2 * (path_at(t_own) + __popcll(above)) + is_q);
+      uint32_t at = smem_addr(coef + is_q * plane + path_at(t_own) + __popcll(above));
 #pragma unroll 1
       for (int c = 0; c < R; c += 16) {
         const uint32_t bits = own ? (uint32_t)(above >> c) & 0xffffu : 0u;
@@ -402,7 +422,7 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const uint32_t bit = bits >> e & 1u;
-          at -= 8 * bit;
+          at -= 4 * bit;
           store_if(bit, at, __uint_as_float(w[e]));
         }
         if (__any_sync(0xffffffffu, diag)) {
@@ -455,30 +475,27 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
     if (st == stages - 1 && own) {  // the decays along the path, while the state is on its way
       float d = gate[t_own];
       const int m = __popcll(above), first = path_at(t_own);
-      uint64_t left = above;
-      for (int i = 0; i < m; i += 4) {
-        float c[4], gs[4];
-        int s[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          s[e] = left ? 63 - __clzll((long long)left) : 0;
-          left &= ~(1ull << s[e]);
-          c[e] = coef[2 * (first + i + e) + is_q];
-          gs[e] = gate[s[e]];
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (i + e < m) {
-            c[e] *= d;
-            d *= gs[e];
-            if (i == 0) reinterpret_cast<float*>(node[t_own].coef + e)[is_q] = c[e];
-            else coef[2 * (first + i + e) + is_q] = c[e];
-            if (!is_q) place[first + i + e] = (unsigned char)s[e];
-          }
-      }
+      float4* c4 = reinterpret_cast<float4*>(coef + is_q * plane + first);
+      auto scale4 = [&](float4 c, uint32_t w, int left) {  // the gates of absent entries are not taken
+        const float g0 = gate[w & 255u], g1 = gate[w >> 8 & 255u], g2 = gate[w >> 16 & 255u], g3 = gate[w >> 24];
+        c.x = left > 0 ? c.x * d : 0.0f;
+        d = left > 0 ? d * g0 : d;
+        c.y = left > 1 ? c.y * d : 0.0f;
+        d = left > 1 ? d * g1 : d;
+        c.z = left > 2 ? c.z * d : 0.0f;
+        d = left > 2 ? d * g2 : d;
+        c.w = left > 3 ? c.w * d : 0.0f;
+        d = left > 3 ? d * g3 : d;
+        return c;
+      };
+      *reinterpret_cast<float4*>(node[t_own].coef[is_q]) = scale4(c4[0], four, m);
+      for (int i = 4; i < m; i += 4)
+        c4[i >> 2] = scale4(c4[i >> 2], *reinterpret_cast<const uint32_t*>(place + first + i), m - i);
       if (!is_q) {
         node[t_own].gamma = d;
-        finish(t_own, m);
+        node[t_own].path = m | first << 14 | (m > 4 ? 1 << 31 : 0);
+        *reinterpret_cast<uint4*>(node[t_own].at) =
+            make_uint4((four & 255u) * (DV * 4), (four >> 8 & 255u) * (DV * 4), (four >> 16 & 255u) * (DV * 4), (four >> 24) * (DV * 4));
       }
     }
     if constexpr (TS == 1) cp_async_wait<0>();
@@ -506,8 +523,9 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
 
   if (!failed && tid < DV) {
     uint32_t mine_k = umma::taddr(tmem, warp * 32, 0), mine_q = mine_k + R;
-    const float4* entry = reinterpret_cast<const float4*>(coef);       // two entries each
-    const uint32_t* places = reinterpret_cast<const uint32_t*>(place);  // four
+    const float4* entry_u = reinterpret_cast<const float4*>(coef);           // four entries each
+    const float4* entry_o = reinterpret_cast<const float4*>(coef + plane);
+    const uint32_t* places = reinterpret_cast<const uint32_t*>(place);
     const unsigned char* rows_u = reinterpret_cast<const unsigned char*>(U + tid);
     float* mine = U + tid;
     IT* go = static_cast<IT*>(p.o) + base_v + tid;
@@ -522,20 +540,17 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
     auto row = [&](uint32_t at) { return *reinterpret_cast<const float*>(rows_u + at); };
     auto further = [&](int path, float& pred, float& out) {
       const int m = path & 255;
-      const float4* en = entry + 2 * (path >> 16 & 0x7fff);
-      const uint32_t* pl = places + (path >> 16 & 0x7fff);
+      const int first = path >> 16 & 0x7fff, last = first + ((m - 1) >> 2);
 #pragma unroll 1
-      for (int i = 4; i < m; i += 4) {
-        en += 2;
-        ++pl;
-        const float4 c0 = en[0], c1 = en[1];
-        const uint32_t s = *pl;
+      for (int i = first + 1; i <= last; ++i) {
+        const float4 cu = entry_u[i], co = entry_o[i];
+        const uint32_t s = places[i];
         const float x0 = row((s & 255u) * (DV * 4)), x1 = row((s >> 8 & 255u) * (DV * 4));
         const float x2 = row((s >> 16 & 255u) * (DV * 4)), x3 = row((s >> 24) * (DV * 4));
-        pred = fmaf(c0.x, x0, pred), out = fmaf(c0.y, x0, out);
-        pred = fmaf(c0.z, x1, pred), out = fmaf(c0.w, x1, out);
-        pred = fmaf(c1.x, x2, pred), out = fmaf(c1.y, x2, out);
-        pred = fmaf(c1.z, x3, pred), out = fmaf(c1.w, x3, out);
+        pred = fmaf(cu.x, x0, pred), out = fmaf(co.x, x0, out);
+        pred = fmaf(cu.y, x1, pred), out = fmaf(co.y, x1, out);
+        pred = fmaf(cu.z, x2, pred), out = fmaf(co.z, x2, out);
+        pred = fmaf(cu.w, x3, pred), out = fmaf(co.w, x3, out);
       }
     };
     umma::wait_ld();
@@ -544,20 +559,20 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
       asm volatile("" : "+r"(k0), "+r"(k1), "+r"(q0), "+r"(q1));  // not before the wait
       const float4 ia = reinterpret_cast<const float4*>(rec)[0], ib = reinterpret_cast<const float4*>(rec)[4];
       const uint4 oa = reinterpret_cast<const uint4*>(rec)[1], ob = reinterpret_cast<const uint4*>(rec)[5];
-      const float4 a0 = reinterpret_cast<const float4*>(rec)[2], a1 = reinterpret_cast<const float4*>(rec)[3];
-      const float4 b0 = reinterpret_cast<const float4*>(rec)[6], b1 = reinterpret_cast<const float4*>(rec)[7];
+      const float4 ua = reinterpret_cast<const float4*>(rec)[2], oa4 = reinterpret_cast<const float4*>(rec)[3];
+      const float4 ub = reinterpret_cast<const float4*>(rec)[6], ob4 = reinterpret_cast<const float4*>(rec)[7];
       const float va = mine[0], vb = mine[DV];
       const float xa0 = row(oa.x), xa1 = row(oa.y), xa2 = row(oa.z), xa3 = row(oa.w);
       const float xb0 = row(ob.x), xb1 = row(ob.y), xb2 = row(ob.z), xb3 = row(ob.w);
       float preda = ia.x * __uint_as_float(k0), outa = ia.x * __uint_as_float(q0);
       float predb = ib.x * __uint_as_float(k1), outb = ib.x * __uint_as_float(q1);
-      preda = fmaf(a0.x, xa0, preda), outa = fmaf(a0.y, xa0, outa);
-      predb = fmaf(b0.z, xb1, predb), outb = fmaf(b0.w, xb1, outb);
-      preda = fmaf(a0.z, xa1, preda), outa = fmaf(a0.w, xa1, outa);
-      predb = fmaf(b1.x, xb2, predb), outb = fmaf(b1.y, xb2, outb);
-      preda = fmaf(a1.x, xa2, preda), outa = fmaf(a1.y, xa2, outa);
-      predb = fmaf(b1.z, xb3, predb), outb = fmaf(b1.w, xb3, outb);
-      preda = fmaf(a1.z, xa3, preda), outa = fmaf(a1.w, xa3, outa);
+      preda = fmaf(ua.x, xa0, preda), outa = fmaf(oa4.x, xa0, outa);
+      predb = fmaf(ub.y, xb1, predb), outb = fmaf(ob4.y, xb1, outb);
+      preda = fmaf(ua.y, xa1, preda), outa = fmaf(oa4.y, xa1, outa);
+      predb = fmaf(ub.z, xb2, predb), outb = fmaf(ob4.z, xb2, outb);
+      preda = fmaf(ua.z, xa2, preda), outa = fmaf(oa4.z, xa2, outa);
+      predb = fmaf(ub.w, xb3, predb), outb = fmaf(ob4.w, xb3, outb);
+      preda = fmaf(ua.w, xa3, preda), outa = fmaf(oa4.w, xa3, outa);
       const int pa = __float_as_int(ia.w), pb = __float_as_int(ib.w);
       if ((pa | pb) < 0) {
         further(pa, preda, outa);
@@ -566,7 +581,7 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
       const float xa = p.predicts ? ia.y * (va - preda) : va;
       // the second node may continue the first
       const float xp = ob.x == (uint32_t)t * (DV * 4) ? xa : xb0;
-      predb = fmaf(b0.x, xp, predb), outb = fmaf(b0.y, xp, outb);
+      predb = fmaf(ub.x, xp, predb), outb = fmaf(ob4.x, xp, outb);
       const float xb = p.predicts ? ib.y * (vb - predb) : vb;
       mine_k += 2;
       mine_q += 2;
