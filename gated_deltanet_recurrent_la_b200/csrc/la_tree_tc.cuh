@@ -411,11 +411,12 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
     if (warp < 4 && warp * 32 < 2 * R) {
       // nearest first: the places fall as s rises
       uint32_t at = smem_addr(coef + is_q * plane + path_at(t_own) + __popcll(above));
+      const uint32_t at_self = smem_addr(&node[t_own].self);
 #pragma unroll 1
       for (int c = 0; c < R; c += 16) {
         const uint32_t bits = own ? (uint32_t)(above >> c) & 0xffffu : 0u;
-        const bool diag = own && is_q && t_own >> 4 == c >> 4;
-        if (!__any_sync(0xffffffffu, bits || diag)) continue;
+        const uint32_t diag = own && is_q && t_own >> 4 == c >> 4 ? 1u << (t_own & 15) : 0u;
+        if (!__any_sync(0xffffffffu, bits | diag)) continue;
         uint32_t w[16];
         umma::ld16(umma::taddr(tmem, warp * 32, c), w);
         umma::wait_ld();
@@ -426,10 +427,8 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
           store_if(bit, at, __uint_as_float(w[e]));
         }
         if (__any_sync(0xffffffffu, diag)) {
-          uint32_t self = 0;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) self = (t_own & 15) == e ? w[e] : self;
-          if (diag) node[t_own].self = __uint_as_float(self);
+          for (int e = 0; e < 16; ++e) store_if(diag >> e & 1u, at_self, __uint_as_float(w[e]));
         }
       }
     }
