@@ -91,7 +91,7 @@ struct RowPieces {
 };
 
 template <typename IT>
-__global__ void __launch_bounds__(kRowThreads) beam_row_kernel(const BeamParams p, int parts) {
+__global__ void __launch_bounds__(kRowThreads, 3) beam_row_kernel(const BeamParams p, int parts) {
   constexpr int E = RowPieces<IT>::E;
   __shared__ uint64_t keys[kRowThreads];  // the threads' best, then the groups', then the candidates
   __shared__ double sums[kRowThreads / 32];
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kRowThreads) beam_row_kernel(const BeamParams 
     if (top > -INFINITY) {
       float s = 0.0f;
 #pragma unroll
-      for (int e = 0; e < E; ++e) s += expf(f[e] - top);
+      for (int e = 0; e < E; ++e) s += __expf(f[e] - top);
       sum += (double)s;
     }
   };

@@ -78,6 +78,49 @@ __device__ __forceinline__ int tree_span(const int32_t* cu, int total, int max_n
 }
 __device__ __forceinline__ uint32_t span_error(int n) { return n == -1 ? LA_DEVERR_CU_SEQLENS : LA_DEVERR_TREE; }
 
+// The same in two steps: the piece as it lies in memory, and its values.
+template <typename ST>
+struct RawPiece {
+  uint4 w;
+};
+template <>
+struct RawPiece<q8_t> {
+  uint4 w;      // BF16 values, or codes in w.x, w.y
+  float scale;  // negative: BF16
+};
+template <typename ST, int DV>
+__device__ __forceinline__ RawPiece<ST> raw_piece(const TileReader<ST>& S, int i, int c) {
+  RawPiece<ST> r;
+  if constexpr (std::is_same<ST, q8_t>::value) {
+    constexpr int NG = DV / 32;
+    const int e = S.row_info[i], idx = e >> 1;
+    if (e & 1) {
+      r.w = __ldcs(reinterpret_cast<const uint4*>(S.tile + S.n8 * DV + S.n8 * NG * 4 + (idx * DV + 8 * c) * 2));
+      r.scale = -1.0f;
+    } else {
+      const uint2 w = __ldcs(reinterpret_cast<const uint2*>(S.tile + idx * DV + 8 * c));
+      r.w = make_uint4(w.x, w.y, 0u, 0u);
+      r.scale = reinterpret_cast<const float*>(S.tile + S.n8 * DV)[idx * NG + (c >> 2)];
+    }
+  } else {
+    r.w = __ldcs(reinterpret_cast<const uint4*>(S.tile + i * DV) + c);
+  }
+  return r;
+}
+template <typename ST>
+__device__ __forceinline__ void unpack_piece(const RawPiece<ST>& r, float* x) {
+  if constexpr (std::is_same<ST, q8_t>::value) {
+    if (r.scale < 0.0f) {
+      StateVec<__nv_bfloat16>::unpack(r.w, x);
+    } else {
+      const uint32_t words[2] = {r.w.x, r.w.y};
+      q8_unpack<8>(words, r.scale, x);
+    }
+  } else {
+    StateVec<ST>::unpack(r.w, x);
+  }
+}
+
 // E consecutive state values, piece c of row i (columns E c ..), in FP32; E = 8, or 4 for FP32 states
 template <int E, typename ST, int DV>
 __device__ __forceinline__ void state_piece(const TileReader<ST>& S, int i, int c, float* x) {
@@ -291,6 +334,7 @@ cudaError_t launch_tree(const TreeParams& p, cudaStream_t stream) {
 // group, so a path node costs it one piece of u and one factor per row.
 
 constexpr int kCommitThreads = 256;
+constexpr int kCommitPieces = 2;  // unpacked at a time
 
 // Eight (q8, BF16) or four (FP32) consecutive values of a row.
 template <typename ST>
@@ -303,8 +347,14 @@ __host__ __device__ constexpr int commit_smem(int rows) {
   return 4 * (rows * (DK + DV) + DK + 2 * DK + 4 * rows + 4);
 }
 
+// CTAs of an SM whose raw pieces and working registers fit
+template <typename ST, int SIZE>
+constexpr int commit_ctas() {
+  return SIZE <= 128 * 64 ? 4 : std::is_same<ST, float>::value ? 2 : std::is_same<ST, q8_t>::value ? 3 : 4;
+}
+
 template <typename ST, typename IT, int DK, int DV, bool KDA>
-__global__ void __launch_bounds__(kCommitThreads, 2) commit_kernel(const TreeCommitParams p, int rows) {
+__global__ void __launch_bounds__(kCommitThreads, (commit_ctas<ST, DK * DV>())) commit_kernel(const TreeCommitParams p, int rows) {
   constexpr bool Q8 = std::is_same<ST, q8_t>::value;
   constexpr int E = CommitVec<ST>::kElems, PR = DV / E;            // pieces of a row
   constexpr int NP = DK * PR;
@@ -349,10 +399,10 @@ __global__ void __launch_bounds__(kCommitThreads, 2) commit_kernel(const TreeCom
   const int row0 = tid / PR, col = tid % PR;
   TileReader<ST> S;
   S.init(p.src, (int64_t)rs * H + h, DK, DV, p.n_hp, src_info);
-  float x[NPT][E];
+  RawPiece<ST> raw[NPT];
   if (tid < ACT) {
 #pragma unroll
-    for (int k = 0; k < NPT; ++k) state_piece<E, ST, DV>(S, row0 + k * RS, col, x[k]);
+    for (int k = 0; k < NPT; ++k) raw[k] = raw_piece<ST, DV>(S, row0 + k * RS, col);
   }
   for (int t = tid; t < n; t += kCommitThreads) par[t] = __ldg(p.parent + c0 + t);
   __syncthreads();
@@ -417,55 +467,65 @@ __global__ void __launch_bounds__(kCommitThreads, 2) commit_kernel(const TreeCom
         p.u + ((int64_t)(c0 + path[e / (DV / 4)]) * H + h) * DV + e % (DV / 4) * 4));
   __syncthreads();
   if (tid >= ACT) return;
-  if (m > 0 && (KDA || p.g)) {
+  // CH pieces at a time: few registers, so that four CTAs of an SM have their tiles in flight (two
+  // for FP32 128 x 128).  64 sequences x 32 heads BF16: 26.4 us, 33.8 with all pieces unpacked at
+  // once and two CTAs.
+  constexpr int CH = NPT < kCommitPieces ? NPT : kCommitPieces;
 #pragma unroll
-    for (int k = 0; k < NPT; ++k) {
-      const float g = G[KDA ? row0 + k * RS : 0];
+  for (int k0 = 0; k0 < NPT; k0 += CH) {
+    float x[CH][E];
 #pragma unroll
-      for (int e = 0; e < E; ++e) x[k][e] *= g;
-    }
-  }
-  for (int a = 0; a < m; ++a) {
-    float y[E];
+    for (int k = 0; k < CH; ++k) {
+      unpack_piece(raw[k0 + k], x[k]);
+      if (m > 0 && (KDA || p.g)) {
+        const float g = G[KDA ? row0 + (k0 + k) * RS : 0];
 #pragma unroll
-    for (int e = 0; e < E; e += 4) {
-      const float4 w = *reinterpret_cast<const float4*>(us + a * DV + col * E + e);
-      y[e] = w.x; y[e + 1] = w.y; y[e + 2] = w.z; y[e + 3] = w.w;
-    }
-#pragma unroll
-    for (int k = 0; k < NPT; ++k) {
-      const float f = kc[a * DK + row0 + k * RS];
-#pragma unroll
-      for (int e = 0; e < E; ++e) x[k][e] = fmaf(f, y[e], x[k][e]);
-    }
-  }
-  if constexpr (Q8) {
-    constexpr int NG = DV / 32;
-    const int n8 = DK - p.n_hp;
-    unsigned char* tile = static_cast<unsigned char*>(p.dst) + ((int64_t)ws * H + h) * q8_tile_bytes(DK, DV, p.n_hp);
-#pragma unroll
-    for (int k = 0; k < NPT; ++k) {
-      const int e = dst_info[row0 + k * RS], idx = e >> 1;
-      float amax = 0.0f;
-#pragma unroll
-      for (int c = 0; c < 8; ++c) amax = fmaxf(amax, fabsf(x[k][c]));
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));  // 32 columns: four threads
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      if (e & 1) {
-        reinterpret_cast<uint4*>(tile + n8 * DV + n8 * NG * 4)[idx * PR + col] = StateVec<__nv_bfloat16>::pack(x[k]);
-      } else {
-        float s, inv;
-        q8_scales(amax, s, inv);
-        uint32_t words[2];
-        q8_pack<8>(x[k], inv, words);
-        reinterpret_cast<uint2*>(tile)[idx * PR + col] = make_uint2(words[0], words[1]);
-        if ((col & 3) == 0) reinterpret_cast<float*>(tile + n8 * DV)[idx * NG + (col >> 2)] = s;
+        for (int e = 0; e < E; ++e) x[k][e] *= g;
       }
     }
-  } else {
-    uint4* tile = reinterpret_cast<uint4*>(static_cast<ST*>(p.dst) + ((int64_t)ws * H + h) * DK * DV);
+#pragma unroll 1
+    for (int a = 0; a < m; ++a) {
+      float y[E];
 #pragma unroll
-    for (int k = 0; k < NPT; ++k) __stcs(tile + (row0 + k * RS) * PR + col, StateVec<ST>::pack(x[k]));
+      for (int e = 0; e < E; e += 4) {
+        const float4 w = *reinterpret_cast<const float4*>(us + a * DV + col * E + e);
+        y[e] = w.x; y[e + 1] = w.y; y[e + 2] = w.z; y[e + 3] = w.w;
+      }
+#pragma unroll
+      for (int k = 0; k < CH; ++k) {
+        const float f = kc[a * DK + row0 + (k0 + k) * RS];
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[k][e] = fmaf(f, y[e], x[k][e]);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      const int row = row0 + (k0 + k) * RS;
+      if constexpr (Q8) {
+        constexpr int NG = DV / 32;
+        const int n8 = DK - p.n_hp;
+        unsigned char* tile = static_cast<unsigned char*>(p.dst) + ((int64_t)ws * H + h) * q8_tile_bytes(DK, DV, p.n_hp);
+        const int e = dst_info[row], idx = e >> 1;
+        float amax = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) amax = fmaxf(amax, fabsf(x[k][c]));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));  // 32 columns: four threads
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        if (e & 1) {
+          reinterpret_cast<uint4*>(tile + n8 * DV + n8 * NG * 4)[idx * PR + col] = StateVec<__nv_bfloat16>::pack(x[k]);
+        } else {
+          float s, inv;
+          q8_scales(amax, s, inv);
+          uint32_t words[2];
+          q8_pack<8>(x[k], inv, words);
+          reinterpret_cast<uint2*>(tile)[idx * PR + col] = make_uint2(words[0], words[1]);
+          if ((col & 3) == 0) reinterpret_cast<float*>(tile + n8 * DV)[idx * NG + (col >> 2)] = s;
+        }
+      } else {
+        uint4* tile = reinterpret_cast<uint4*>(static_cast<ST*>(p.dst) + ((int64_t)ws * H + h) * DK * DV);
+        __stcs(tile + row * PR + col, StateVec<ST>::pack(x[k]));
+      }
+    }
   }
 }
 
