@@ -7,8 +7,10 @@
 // rounding of a sum of their size, and their order decides whole numbers.
 //
 // beam_row_kernel reads a row (or a part of it, where rows are few) once from memory: each
-// thread keeps its running maximum, the sum of exponentials below it, and the key of its best
-// element.  The threads form 128 groups; the n_out-th best of the groups' best elements is at
+// thread keeps the place of its best 16-byte piece and a sum of exponentials against a reference
+// that follows the maximum loosely (they stay below e^8, and it seldom moves).  NaN and +inf show
+// in a piece's maximum or sum and send it to a slower form, so nothing is cleaned element by
+// element: about 50 instructions a piece of eight.  The threads form 128 groups; the n_out-th best of the groups' best elements is at
 // or below the row's n_out-th best element, and elements at or above it lie in n_out groups
 // only, so a second look (from L2) at those few per cent of the row finds every candidate:
 // n_out of them and a handful more, which are ranked by counting.  beam_merge_kernel joins the
@@ -27,8 +29,8 @@ constexpr int kMaxParts = 16;
 static_assert(kGroups >= LA_BEAM_MAX && kCand <= kRowThreads && kRowThreads % kGroups == 0, "sizes");
 
 struct BeamPart {   // of one part of a row: then n_out keys (order of the logit, ~index), best first; 0 = none
-  double sum;       // of exp(x - top)
-  float top;
+  double sum;       // of exp(x - ref)
+  float ref;        // -inf: nothing
   float pad;
 };
 __host__ __device__ constexpr int64_t beam_part_bytes(int n_out) { return (int64_t)sizeof(BeamPart) + 8 * (int64_t)n_out; }
@@ -83,6 +85,16 @@ struct RowPieces {
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
+  // of the piece's values f = unpack(w): NaN counts as nothing unless all are
+  static __device__ __forceinline__ float largest(const uint4& w, const float* f) {
+    if constexpr (sizeof(IT) == 4) {
+      return fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3]));
+    } else {
+      const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&w);
+      const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+      return fmaxf(__low2float(m), __high2float(m));
+    }
+  }
   static __device__ __forceinline__ void values(const uint4& w, float* f) {
     StateVec<IT>::unpack(w, f);
 #pragma unroll
@@ -90,12 +102,20 @@ struct RowPieces {
   }
 };
 
+// 2^x to about 2^-22 of its value, 0 for results below 2^-126
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 template <typename IT>
 __global__ void __launch_bounds__(kRowThreads, 3) beam_row_kernel(const BeamParams p, int parts) {
   constexpr int E = RowPieces<IT>::E;
   __shared__ uint64_t keys[kRowThreads];  // the threads' best, then the groups', then the candidates
   __shared__ double sums[kRowThreads / 32];
   __shared__ float tops[kRowThreads / 32];
+  __shared__ int ranks[kGroups];
   __shared__ int winners[LA_BEAM_MAX];
   __shared__ uint64_t tau;
   __shared__ int n_win, n_cand;
@@ -123,36 +143,41 @@ __global__ void __launch_bounds__(kRowThreads, 3) beam_row_kernel(const BeamPara
   const int span = (p.vocab + parts - 1) / parts, lo = part * span, hi = min(p.vocab, lo + span);
   const RowPieces<IT> pieces(static_cast<const IT*>(p.logits) + (int64_t)row * p.row_stride, lo, hi);
 
-  float top = -INFINITY, at = -INFINITY;
-  int where = -1;
+  float ref = -INFINITY, at = -INFINITY;
+  int where = -1;  // piece of the thread's first largest element, `at`
   double sum = 0.0;
-  auto visit = [&](const uint4& w, int j) {
-    float f[E];
-    RowPieces<IT>::values(w, f);
-    float m = f[0];
-#pragma unroll
-    for (int e = 1; e < E; ++e) m = fmaxf(m, f[e]);
-    if (m > at || where < 0) {  // the first of the thread's largest elements
-      const int v0 = pieces.first + j * E;
-      int first = -1;
-#pragma unroll
-      for (int e = E - 1; e >= 0; --e)
-        if (f[e] == m && pieces.has(v0 + e)) first = v0 + e;
-      if (first >= 0) {
-        at = m;
-        where = first;
-      }
+  auto follow = [&](float m, int j) {  // m: the piece's maximum, finite or -inf
+    if (m > at || where < 0) {
+      at = m;
+      where = j;
     }
-    if (m > top) {
-      sum *= (double)expf(top - m);
-      top = m;
+    if (m > ref + 8.0f) {
+      sum *= (double)expf(ref - m);
+      ref = m;
     }
-    if (top > -INFINITY) {
-      float s = 0.0f;
+  };
+  // of x - ref, rounded once before 2^.. (an offset of all logits cancels exactly)
+  auto exponential = [&](float x) { return exp2_approx((x - ref) * 1.44269504f); };
+  auto visit = [&](const uint4& w, int j) -> float {  // the piece's exponentials
+    float f[E], s = 0.0f;
+    StateVec<IT>::unpack(w, f);
+    const float m = RowPieces<IT>::largest(w, f);
+    if (m < INFINITY) {
+      follow(m, j);
 #pragma unroll
-      for (int e = 0; e < E; ++e) s += __expf(f[e] - top);
-      sum += (double)s;
+      for (int e = 0; e < E; ++e) s += exponential(f[e]);
+      if (s < INFINITY) return s;
     }
+    RowPieces<IT>::values(w, f);  // a NaN or +inf among them, or nothing finite so far
+    float c = f[0];
+#pragma unroll
+    for (int e = 1; e < E; ++e) c = fmaxf(c, f[e]);
+    follow(c, j);
+    s = 0.0f;
+    if (ref > -INFINITY)
+#pragma unroll
+      for (int e = 0; e < E; ++e) s += exponential(f[e]);
+    return s;
   };
   int j = tid;
   for (; j + 3 * kRowThreads < pieces.n; j += 4 * kRowThreads) {  // four pieces in flight
@@ -160,23 +185,36 @@ __global__ void __launch_bounds__(kRowThreads, 3) beam_row_kernel(const BeamPara
 #pragma unroll
     for (int e = 0; e < 4; ++e) w[e] = pieces.load(j + e * kRowThreads);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) visit(w[e], j + e * kRowThreads);
+    for (int e = 0; e < 4; ++e) sum += (double)visit(w[e], j + e * kRowThreads);
   }
-  for (; j < pieces.n; j += kRowThreads) visit(pieces.load(j), j);
+  for (; j < pieces.n; j += kRowThreads) sum += (double)visit(pieces.load(j), j);
 
-  keys[tid] = where < 0 ? 0ull : beam_key(at, where);
+  keys[tid] = 0ull;
+  if (where >= 0) {  // the first of the piece's largest elements
+    float f[E];
+    RowPieces<IT>::values(pieces.load(where), f);
+    int first = -1;
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    const float t = __shfl_xor_sync(0xffffffffu, top, off);
-    const double s = __shfl_xor_sync(0xffffffffu, sum, off);
-    const float m = fmaxf(top, t);
-    if (m > -INFINITY) sum = sum * (double)expf(top - m) + s * (double)expf(t - m);
-    top = m;
+    for (int e = E - 1; e >= 0; --e)
+      if (f[e] == at && pieces.has(pieces.first + where * E + e)) first = pieces.first + where * E + e;
+    if (first >= 0) keys[tid] = beam_key(at, first);
   }
+  // the sums against the largest reference of a warp, then of the CTA
+  auto join = [&](float& r, double& x) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+      const float r2 = __shfl_xor_sync(0xffffffffu, r, off), to = fmaxf(r, r2);
+      const double x2 = __shfl_xor_sync(0xffffffffu, x, off);
+      if (to > -INFINITY) x = x * (double)expf(r - to) + x2 * (double)expf(r2 - to);
+      r = to;
+    }
+  };
+  join(ref, sum);
   if (lane == 0) {
-    tops[warp] = top;
+    tops[warp] = ref;
     sums[warp] = sum;
   }
+  if (tid < kGroups) ranks[tid] = 0;
   if (tid == 0) {
     tau = 0ull;
     n_cand = n_win = 0;
@@ -186,21 +224,26 @@ __global__ void __launch_bounds__(kRowThreads, 3) beam_row_kernel(const BeamPara
   if (tid < kGroups) {
 #pragma unroll
     for (int e = 0; e < kRowThreads / kGroups; ++e) mine = max(mine, keys[tid + e * kGroups]);
-  } else if (tid == kGroups) {
-    float m = tops[0];
-    for (int w = 1; w < kRowThreads / 32; ++w) m = fmaxf(m, tops[w]);
-    double s = 0.0;
-    if (m > -INFINITY)
-      for (int w = 0; w < kRowThreads / 32; ++w) s += sums[w] * (double)expf(tops[w] - m);
-    *head = BeamPart{s, m, 0.0f};
+  } else if (warp == kGroups / 32) {
+    float r = lane < kRowThreads / 32 ? tops[lane] : -INFINITY;
+    double x = lane < kRowThreads / 32 ? sums[lane] : 0.0;
+    join(r, x);
+    if (lane == 0) *head = BeamPart{x, r, 0.0f};
   }
   __syncthreads();
   if (tid < kGroups) keys[tid] = mine;
   __syncthreads();
-  if (tid < kGroups && mine) {
+  {  // ranks of the groups' best: every thread compares with a quarter of them
+    constexpr int kShare = kGroups * kGroups / kRowThreads;
+    const uint64_t k = keys[tid % kGroups];
     int rank = 0;
 #pragma unroll 8
-    for (int g = 0; g < kGroups; ++g) rank += keys[g] > mine;
+    for (int g = 0; g < kShare; ++g) rank += keys[tid / kGroups * kShare + g] > k;
+    if (rank) atomicAdd(&ranks[tid % kGroups], rank);
+  }
+  __syncthreads();
+  if (tid < kGroups && mine) {
+    const int rank = ranks[tid];
     if (rank < take) {
       winners[rank] = tid;
       atomicAdd(&n_win, 1);
@@ -293,16 +336,16 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
   if (tid < K) {
     const float cum = p.cum[(int64_t)b * K + tid];
     const unsigned char* w = first + (int64_t)tid * parts * pb;
-    float top = -INFINITY;
-    for (int s = 0; s < parts; ++s) top = fmaxf(top, reinterpret_cast<const BeamPart*>(w + s * pb)->top);
+    float ref = -INFINITY;
+    for (int s = 0; s < parts; ++s) ref = fmaxf(ref, reinterpret_cast<const BeamPart*>(w + s * pb)->ref);
     double off = cum > -INFINITY ? (double)fminf(cum, 3.402823466e38f) : 0.0;
-    if (top > -INFINITY) {  // (a dead or finished beam has no top)
+    if (ref > -INFINITY) {  // (a dead or finished beam, or one with every token masked, has none)
       double sum = 0.0;
       for (int s = 0; s < parts; ++s) {
         const BeamPart* q = reinterpret_cast<const BeamPart*>(w + s * pb);
-        sum += q->sum * exp((double)q->top - (double)top);
+        sum += q->sum * (double)expf(q->ref - ref);
       }
-      off -= (double)top + log(sum);
+      off -= (double)ref + log(sum);
     }
     offset[tid] = off;
   }
