@@ -254,7 +254,7 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
   uint32_t four = 0x01010101u * R;  // the nearest four, R where there are fewer
   const bool is_q = tid >= R;
   const int t_own = is_q ? tid - R : tid;
-  const bool own = !KDA && tid < 2 * R && t_own < n;
+  const bool own = tid < (KDA ? R : 2 * R) && t_own < n;  // (kda: the walk forms both)
   if (own) {
     uint32_t* words = reinterpret_cast<uint32_t*>(place + path_at(t_own));
     uint32_t word = 0x01010101u * R;
@@ -271,23 +271,18 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
     if (i < 4) four = word;
     if (!is_q && ((i & 3) || i == 0)) *words = word;
   }
-  // For the kda walk and the node behind an odd last one: entries up to the next four (factor 0,
-  // row of zeros), then the record's length and offsets.
-  auto finish = [&](int t, int m) {
-    const int first = path_at(t);
-    for (int i = m; i < path_size(m); ++i) {
-      coef[first + i] = coef[plane + first + i] = 0.0f;
-      place[first + i] = (unsigned char)R;
-    }
-    node[t].path = m | first << 14 | (m > 4 ? 1 << 31 : 0);
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(place + first);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      node[t].at[e] = (w >> (8 * e) & 255) * (DV * 4);
-      if (e >= m) node[t].coef[0][e] = node[t].coef[1][e] = 0.0f;
-    }
+  // length and offsets of a record
+  auto describe = [&](int t, int m, uint32_t w) {
+    node[t].path = m | path_at(t) << 14 | (m > 4 ? 1 << 31 : 0);
+    *reinterpret_cast<uint4*>(node[t].at) =
+        make_uint4((w & 255u) * (DV * 4), (w >> 8 & 255u) * (DV * 4), (w >> 16 & 255u) * (DV * 4), (w >> 24) * (DV * 4));
   };
-  if (tid == 0 && (n & 1)) finish(n, 0);
+  if (own && !is_q) describe(t_own, __popcll(above), four);
+  if (tid == 0 && (n & 1)) {  // the node behind an odd last one: no path
+    describe(n, 0, 0x01010101u * R);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) node[n].coef[e >> 2][e & 3] = 0.0f;
+  }
 
   if constexpr (KDA) {
     // K and g in FP32 behind A; a warp per node walks its path with one decay per channel, forms
@@ -303,64 +298,55 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
     }
     __syncthreads();
     for (int t = warp; t < n; t += NT / 32) {
-      float kt[CH], qt[CH], d[CH];
+      float kt[CH], qt[CH], d[CH], self = 0.0f;
       load_f32<IT, CH>(gq + row0 + t * row_step + lane * CH, qt);
-      float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         kt[c] = Kf[t * DK + lane * CH + c];
         d[c] = Gf[t * DK + lane * CH + c];
-        v[0] = fmaf(qt[c], kt[c], v[0]);
+        self = fmaf(qt[c], kt[c], self);
       }
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
-      if (lane == 0) node[t].self = v[0];
-      float* at = coef + path_at(t);
-      int m = 0;
-      for (int s = par[t]; s >= 0;) {  // two nodes of the path at a time: their reductions overlap
-        const int s2 = par[s];
+      for (int off = 16; off > 0; off >>= 1) self += __shfl_xor_sync(0xffffffffu, self, off);
+      if (lane == 0) node[t].self = self;
+      const int first = path_at(t), m = node[t].path & 255;
+      int i = 0;
+      do {  // four nodes of the path at a time (at least once: the record's coefficients)
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(place + first + i);
+        float v[8];  // (k_t, q_t) . D k of the four
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = 0.0f;
+        for (int e = 0; e < 4; ++e) {
+          v[2 * e] = v[2 * e + 1] = 0.0f;
+          if (i + e < m) {
+            const int s = w >> (8 * e) & 255;
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          const float x = d[c] * Kf[s * DK + lane * CH + c];
-          v[0] = fmaf(kt[c], x, v[0]);
-          v[1] = fmaf(qt[c], x, v[1]);
-          d[c] *= Gf[s * DK + lane * CH + c];
-        }
-        if (s2 >= 0) {
-#pragma unroll
-          for (int c = 0; c < CH; ++c) {
-            const float x = d[c] * Kf[s2 * DK + lane * CH + c];
-            v[2] = fmaf(kt[c], x, v[2]);
-            v[3] = fmaf(qt[c], x, v[3]);
-            d[c] *= Gf[s2 * DK + lane * CH + c];
+            for (int c = 0; c < CH; ++c) {
+              const float x = d[c] * Kf[s * DK + lane * CH + c];
+              v[2 * e] = fmaf(kt[c], x, v[2 * e]);
+              v[2 * e + 1] = fmaf(qt[c], x, v[2 * e + 1]);
+              d[c] *= Gf[s * DK + lane * CH + c];
+            }
           }
         }
+        // eight sums over the lanes with nine shuffles: each step hands half of the values over
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1)
+        for (int half = 4, off = 16; half >= 1; half >>= 1, off >>= 1) {
+          const bool up = lane & off;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] += __shfl_xor_sync(0xffffffffu, v[e], off);
-        if (lane == 0) {
-          at[m] = v[0];
-          at[plane + m] = v[1];
-          place[path_at(t) + m] = (unsigned char)s;
-          if (s2 >= 0) {
-            at[m + 1] = v[2];
-            at[plane + m + 1] = v[3];
-            place[path_at(t) + m + 1] = (unsigned char)s2;
-          }
-          if (m < 4) {
-            node[t].coef[0][m] = v[0];
-            node[t].coef[1][m] = v[1];
-            node[t].coef[0][m + 1] = v[2];
-            node[t].coef[1][m + 1] = v[3];
+          for (int e = 0; e < half; ++e) {
+            const float give = up ? v[e] : v[e + half], keep = up ? v[e + half] : v[e];
+            v[e] = keep + __shfl_xor_sync(0xffffffffu, give, off);
           }
         }
-        m += s2 >= 0 ? 2 : 1;
-        s = s2 >= 0 ? par[s2] : -1;
-      }
-      if (lane == 0) finish(t, m);
+        v[0] += __shfl_xor_sync(0xffffffffu, v[0], 2);
+        v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
+        if ((lane & 3) == 0) {  // value lane / 4: entry lane / 8, of u or of o
+          const int e = lane >> 3, o = lane >> 2 & 1;
+          if (i == 0) node[t].coef[o][e] = v[0];
+          else coef[o * plane + first + i + e] = v[0];
+        }
+        i += 4;
+      } while (i < m);
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         kt[c] *= d[c];
@@ -471,7 +457,7 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
         store_terms<8>(smS + umma::panel_piece(64, at / (DV / 8), at % (DV / 8)), termS, x[e]);
       }
     }
-    if (st == stages - 1 && own) {  // the decays along the path, while the state is on its way
+    if (!KDA && st == stages - 1 && own) {  // the decays along the path, while the state is on its way
       float d = gate[t_own];
       const int m = __popcll(above), first = path_at(t_own);
       float4* c4 = reinterpret_cast<float4*>(coef + is_q * plane + first);
@@ -490,12 +476,7 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
       *reinterpret_cast<float4*>(node[t_own].coef[is_q]) = scale4(c4[0], four, m);
       for (int i = 4; i < m; i += 4)
         c4[i >> 2] = scale4(c4[i >> 2], *reinterpret_cast<const uint32_t*>(place + first + i), m - i);
-      if (!is_q) {
-        node[t_own].gamma = d;
-        node[t_own].path = m | first << 14 | (m > 4 ? 1 << 31 : 0);
-        *reinterpret_cast<uint4*>(node[t_own].at) =
-            make_uint4((four & 255u) * (DV * 4), (four >> 8 & 255u) * (DV * 4), (four >> 16 & 255u) * (DV * 4), (four >> 24) * (DV * 4));
-      }
+      if (!is_q) node[t_own].gamma = d;
     }
     if constexpr (TS == 1) cp_async_wait<0>();
     umma::fence_smem();
