@@ -15,7 +15,10 @@
 // Precision: the accumulators are FP32.  BF16 operands are multiplied exactly; an FP32 operand
 // (FP32 q and k, an FP32 or q8 state, the kda rows scaled by Gamma) is cut into three BF16
 // terms of 8 significand bits each, exact together, and the products of terms i + j <= 2 are
-// summed: what is left out is below 2^-23 of the product.
+// summed: what is left out is below 2^-23 of the product.  An MMA truncates its sum to the FP32
+// accumulator's last place, so the number of MMAs that add to a full-sized accumulator counts:
+// smaller products come first (A K^T) or go to an accumulator of their own (S0^T A^T, whose
+// rows come in stages), which leaves the d_k / 16 of the leading terms.
 //
 // The substitution along the paths is FP32 on the CUDA cores with one thread per column of d_v:
 // it takes S0^T k_t and S0^T q_t from its own tensor-memory lane and keeps its column of V, then
@@ -62,8 +65,13 @@ struct TcCfg {
   // coefficients and a place (the count is a multiple of 8)
   __host__ __device__ static constexpr int entries(int R) { return R * (R + 2) / 2 + 8; }
   static constexpr int smem(int R) { return 1024 + region(R) + entries(R) * 9 + R * 64 + R * 8 + DK * 4 + 32; }
-  // tensor memory: S0^T A^T [2 R], before it A K^T [R]
-  __host__ __device__ static constexpr uint32_t cols(int R) { return R <= 16 ? 32 : R <= 32 ? 64 : 128; }
+  // tensor memory: S0^T A^T [2 R], before it A K^T [R]; with terms, behind it the products of the
+  // smaller ones [2 R]
+  static constexpr bool kTerms = TA * TS > 1;
+  __host__ __device__ static constexpr uint32_t cols(int R) {
+    const int n = kTerms ? 4 * R : 2 * R;
+    return n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : 256;
+  }
 };
 // m entries rounded up to fours, at least one four; the first entry kept for node t
 __device__ __forceinline__ int path_size(int m) { return max(4, (m + 3) & ~3); }
@@ -381,13 +389,13 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
       const uint32_t id = umma::idesc_bf16(128, R, false, false);
       uint32_t acc = 0;
 #pragma unroll
-      for (int i = 0; i < TA; ++i)
+      for (int ij = TA - 1; ij >= 0; --ij)  // the smallest first
 #pragma unroll
-        for (int j = 0; j < TA - i; ++j)
+        for (int i = 0; i <= ij; ++i)
 #pragma unroll
           for (int kk = 0; kk < DK / 16; ++kk) {
             const uint32_t ko = (kk >> 2) * panelA + (kk & 3) * 32;
-            umma::mma(tmem, umma::sdesc_add(dA, i * PA * panelA + ko), umma::sdesc_add(dA, j * PA * panelA + ko), id, acc);
+            umma::mma(tmem, umma::sdesc_add(dA, i * PA * panelA + ko), umma::sdesc_add(dA, (ij - i) * PA * panelA + ko), id, acc);
             acc = 1;
           }
       umma::commit(bar);
@@ -424,16 +432,21 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
   auto issue = [&](int st) {
     umma::fence_after();
     const uint32_t id = umma::idesc_bf16(128, 2 * R, true, false);
+    uint32_t small = st;  // whether something is in their accumulator
 #pragma unroll
-    for (int i = 0; i < TA; ++i)
+    for (int ij = 2; ij >= 0; --ij)
 #pragma unroll
-      for (int j = 0; j < TS; ++j)
-        if (i + j <= 2)
+      for (int i = 0; i <= ij; ++i) {
+        const int j = ij - i;
+        if (i < TA && j < TS) {
           for (int kk = 0; kk < rows / 16; ++kk) {
             const int ka = st * (rows / 16) + kk;
-            umma::mma(tmem, umma::sdesc_add(dS, j * termS + kk * 2048),
-                      umma::sdesc_add(dA, (i * PA + (ka >> 2)) * panelA + (ka & 3) * 32), id, st | i | j | kk);
+            umma::mma(ij ? tmem + 2 * R : tmem, umma::sdesc_add(dS, j * termS + kk * 2048),
+                      umma::sdesc_add(dA, (i * PA + (ka >> 2)) * panelA + (ka & 3) * 32), id, ij ? small : st | kk);
+            if (ij) small = 1;
           }
+        }
+      }
     umma::commit(bar + 1);
   };
   for (int st = 0; st < stages; ++st) {
@@ -514,9 +527,16 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
     const uint32_t step = (uint32_t)step_v;  // (the host has checked that 64 rows of all heads fit 32 bits)
     const bool store_u = p.u != nullptr;
     const NodeRecord* rec = node;
-    uint32_t k0, k1, q0, q1;
-    tmem_ld2(mine_k, k0, k1);
-    tmem_ld2(mine_q, q0, q1);
+    uint32_t k0, k1, q0, q1, kl0 = 0, kl1 = 0, ql0 = 0, ql1 = 0;  // (l: of the smaller terms)
+    auto products = [&] {
+      tmem_ld2(mine_k, k0, k1);
+      tmem_ld2(mine_q, q0, q1);
+      if constexpr (C::kTerms) {
+        tmem_ld2(mine_k + 2 * R, kl0, kl1);
+        tmem_ld2(mine_q + 2 * R, ql0, ql1);
+      }
+    };
+    products();
     auto row = [&](uint32_t at) { return *reinterpret_cast<const float*>(rows_u + at); };
     auto further = [&](int path, float& pred, float& out) {
       const int m = path & 255;
@@ -537,6 +557,13 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
 #pragma unroll 1
     for (int t = 0; t < n; t += 2) {
       asm volatile("" : "+r"(k0), "+r"(k1), "+r"(q0), "+r"(q1));  // not before the wait
+      if constexpr (C::kTerms) {
+        asm volatile("" : "+r"(kl0), "+r"(kl1), "+r"(ql0), "+r"(ql1));
+        k0 = __float_as_uint(__uint_as_float(k0) + __uint_as_float(kl0));
+        k1 = __float_as_uint(__uint_as_float(k1) + __uint_as_float(kl1));
+        q0 = __float_as_uint(__uint_as_float(q0) + __uint_as_float(ql0));
+        q1 = __float_as_uint(__uint_as_float(q1) + __uint_as_float(ql1));
+      }
       const float4 ia = reinterpret_cast<const float4*>(rec)[0], ib = reinterpret_cast<const float4*>(rec)[4];
       const uint4 oa = reinterpret_cast<const uint4*>(rec)[1], ob = reinterpret_cast<const uint4*>(rec)[5];
       const float4 ua = reinterpret_cast<const float4*>(rec)[2], oa4 = reinterpret_cast<const float4*>(rec)[3];
@@ -565,10 +592,7 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
       const float xb = p.predicts ? ib.y * (vb - predb) : vb;
       mine_k += 2;
       mine_q += 2;
-      if (t + 2 < n) {  // a pair ahead of its use
-        tmem_ld2(mine_k, k0, k1);
-        tmem_ld2(mine_q, q0, q1);
-      }
+      if (t + 2 < n) products();  // a pair ahead of its use
       mine[0] = xa;
       mine[DV] = xb;
       // (behind an odd last node: that node once more, instead of a branch)
