@@ -64,7 +64,8 @@ struct TcCfg {
   // paths: entries (at most t for node t, rounded up to fours, four for node 0) as two
   // coefficients and a place (the count is a multiple of 8)
   __host__ __device__ static constexpr int entries(int R) { return R * (R + 2) / 2 + 8; }
-  static constexpr int smem(int R) { return 1024 + region(R) + entries(R) * 9 + R * 64 + R * 8 + DK * 4 + 32; }
+  static constexpr int kRowInfo = std::is_same<ST, q8_t>::value ? DK : 0;
+  static constexpr int smem(int R) { return region(R) + entries(R) * 9 + R * 64 + R * 8 + kRowInfo * 4 + 32; }
   // tensor memory: S0^T A^T [2 R], before it A K^T [R]; with terms, behind it the products of the
   // smaller ones [2 R]
   static constexpr bool kTerms = TA * TS > 1;
@@ -153,9 +154,8 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
     tree_tc_kernel(const TreeParams p, int R) {
   using C = TcCfg<ST, IT, DK, DV, KDA>;
   constexpr int TA = C::TA, TS = C::TS, PA = C::PA, NT = C::kThreads;
-  extern __shared__ __align__(16) unsigned char raw[];
-  // (an offset, not a rounded address: the compiler has to see that this is shared memory)
-  unsigned char* sm = raw + ((0u - smem_addr(raw)) & 1023u);
+  extern __shared__ __align__(1024) unsigned char tc_smem[];  // (not a rounded pointer: it has to be seen as shared memory)
+  unsigned char* sm = tc_smem;
   const int bytesA = C::bytes_a(R), panelA = C::panel_a(R);
   unsigned char* smA = sm;
   unsigned char* smS = sm + bytesA;
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
   float* gate = reinterpret_cast<float*>(place + C::entries(R));     // [R]
   int* par = reinterpret_cast<int*>(gate + R);                       // [R]
   int* row_info = par + R;                                           // [DK] (q8)
-  uint64_t* bar = reinterpret_cast<uint64_t*>(row_info + DK);        // A K^T, S0^T A^T
+  uint64_t* bar = reinterpret_cast<uint64_t*>(row_info + C::kRowInfo);  // A K^T, S0^T A^T
   uint32_t* tm = reinterpret_cast<uint32_t*>(bar + 2);
 
   const int H = p.n_v_heads;
@@ -184,6 +184,10 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
   if (n == 0) return;
   if (slot < 0 || slot >= p.src_slots) {
     if (tid == 0) report(p.err, LA_DEVERR_READ_SLOT);
+    return;
+  }
+  if (smem_addr(sm) & 1023u) {  // the panels' alignment (the declaration asks for it)
+    if (tid == 0) report(p.err, LA_DEVERR_TIMEOUT);
     return;
   }
   int my_par = -1;
