@@ -327,8 +327,11 @@ constexpr int kMergeThreads = 512;
 __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamParams p, int parts) {
   extern __shared__ uint64_t sm[];
   const int b = blockIdx.x, K = p.n_beams, take = min(p.n_out, p.vocab);
-  double* offset = reinterpret_cast<double*>(sm);  // [K]: cum - logsumexp
-  uint64_t* lists = sm + K;                        // [K][take]
+  // score = offset + (x - ref): cum - log(sum) and the reference apart, so that neither is lost
+  // beside logits of 1e38 (a row masked by the type's lowest value is a uniform one)
+  double* offset = reinterpret_cast<double*>(sm);  // [K]
+  double* refs = offset + K;                       // [K]
+  uint64_t* lists = sm + 2 * K;                    // [K][take]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t pb = beam_part_bytes(p.n_out);
   const unsigned char* first = static_cast<const unsigned char*>(p.workspace) + (int64_t)b * K * parts * pb;
@@ -345,9 +348,10 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
         const BeamPart* q = reinterpret_cast<const BeamPart*>(w + s * pb);
         sum += q->sum * (double)expf(q->ref - ref);
       }
-      off -= (double)ref + log(sum);
+      off -= log(sum);
     }
     offset[tid] = off;
+    refs[tid] = ref > -INFINITY ? (double)ref : 0.0;
   }
   if (parts == 1) {
     for (int e = tid; e < K * take; e += kMergeThreads)
@@ -374,10 +378,11 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
   if (warp != 0) return;
   int at[2] = {0, 0};
   uint64_t score[2];
+  auto value = [&](int i, uint64_t k) { return offset[i] + ((double)beam_value((uint32_t)(k >> 32)) - refs[i]); };
   auto load = [&](int e) {
     const int i = lane + 32 * e;
     const uint64_t k = i < K && at[e] < take ? lists[i * take + at[e]] : 0ull;
-    score[e] = k ? score_key(offset[i] + (double)beam_value((uint32_t)(k >> 32))) : 0ull;
+    score[e] = k ? score_key(value(i, k)) : 0ull;
   };
   load(0);
   load(1);
@@ -392,7 +397,7 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
       const int token = (int)(0xffffffffu - (uint32_t)k);
       p.parent[to] = i;
       p.token[to] = token;
-      p.score[to] = (float)(offset[i] + (double)beam_value((uint32_t)(k >> 32)));
+      p.score[to] = (float)value(i, k);
       if (p.finished_out) p.finished_out[to] = (p.finished && p.finished[(int64_t)b * K + i] != 0) || token == p.eos;
       if (w) {
         ++at[1];
@@ -419,7 +424,7 @@ cudaError_t launch_beam_select(const BeamParams& p, cudaStream_t stream) {
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int take = p.n_out < p.vocab ? p.n_out : p.vocab;
-  return launch_dependent(beam_merge_kernel, p.n_seqs, kMergeThreads, 8 * p.n_beams * (1 + take), stream, p, parts);
+  return launch_dependent(beam_merge_kernel, p.n_seqs, kMergeThreads, 8 * p.n_beams * (2 + take), stream, p, parts);
 }
 
 }  // namespace la

@@ -114,10 +114,10 @@ __global__ void __launch_bounds__(kCopyWarps * 32) slab_copy_kernel(const SlabLi
     ++stored;
   };
   int64_t next = me;  // this warp's next piece, counted from the batch's first
-  for (int i0 = 0; i0 < n; i0 += kCopyWarps * 32) {
-    const int i = i0 + (int)threadIdx.x;
+  for (int64_t i0 = 0; i0 < n; i0 += kCopyWarps * 32) {
     int src = -1, dst = -1;
-    if (i < n) {
+    if (i0 + threadIdx.x < n) {
+      const int i = (int)i0 + (int)threadIdx.x;
       if (q.kind == kPairsBeams) {
         uint32_t bad;
         dst = beam_pair(q, i, src, bad);

@@ -493,8 +493,11 @@ la_status la_state_pool_decode(const la_pool *pool, int32_t n, const int32_t *sl
  *   u               device float32 [total_nodes, H_v, d_v], 16-byte aligned, or NULL
  * A sequence without nodes is left alone.  Gates of zero and of either sign are exact (decays
  * are products along the path, never ratios), and a non-finite value reaches only the nodes
- * below it.  FP32 arithmetic; host errors as la_state_step (LA_ERR_UNSUPPORTED for max_nodes
- * above LA_TREE_MAX_NODES, LA_ERR_SHAPE below 1). */
+ * below it.  FP32 arithmetic; the products with the state and among the nodes run on the tensor
+ * cores with FP32 accumulators, BF16 operands exact, FP32 operands to 2^-23 of a product (an
+ * infinite operand may give NaN where FP32 gives an infinity).  Host errors as la_state_step
+ * (LA_ERR_UNSUPPORTED for max_nodes above LA_TREE_MAX_NODES, LA_ERR_SHAPE below 1 and for
+ * H_v d_v LA_TREE_MAX_NODES above UINT32_MAX). */
 #define LA_TREE_MAX_NODES 64
 la_status la_state_tree(la_rule rule, const la_pool *src, const int32_t *read_slot, int32_t n_seqs,
                         const int32_t *cu_nodes, int32_t total_nodes, const int32_t *parent,

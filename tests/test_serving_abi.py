@@ -190,3 +190,8 @@ def test_plain_tree_is_the_oracle_scan_along_every_path(rule, orc):
         np.testing.assert_allclose(o[leaf].numpy(), os_[-1], rtol=0, atol=1e-12)
         state, _ = R.commit_ref(inp, inp["pool"], [leaf], u)
         np.testing.assert_allclose(state.numpy(), S, rtol=0, atol=1e-12)
+
+
+def test_tree_rows_beyond_32_bit_offsets_are_refused(lib):
+    """64 rows of all value heads have to fit 32-bit element offsets."""
+    assert tree(lib, n=1, src=pool(shape=(1, 1 << 19, 128, 128))) == L.LA_ERR_SHAPE
