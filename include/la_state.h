@@ -68,6 +68,8 @@
  *     take them as source and / or destination; the two-launch chunked forms, the
  *     convolution entry points, the kda chunked prefill and la_state_step_qgroups /
  *     la_state_scan_qgroups return LA_ERR_UNSUPPORTED.
+ *     la_state_tree and la_state_tree_commit take them too (the commit as source and
+ *     destination together).
  *   - Pointers to the pool, q, k, v, o and dense buffers must be 16-byte aligned;
  *     g, beta and int32 arrays 4-byte aligned.
  */
