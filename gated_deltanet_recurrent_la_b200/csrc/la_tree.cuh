@@ -21,7 +21,7 @@ namespace tree {
 
 constexpr int kMaxNodes = LA_TREE_MAX_NODES;
 
-// One (pool dtype) element reader of a state tile by (row, column).
+// A state tile of a pool.
 template <typename ST>
 struct TileReader {
   const ST* tile;
@@ -31,25 +31,15 @@ struct TileReader {
   template <int DV>
   __device__ __forceinline__ float at(int i, int j) const { return io_load(tile + i * DV + j); }
 };
-// q8: row_info[i] = rank of row i in its block, times two, plus one for a BF16 row
 template <>
 struct TileReader<q8_t> {
   const unsigned char* tile;
   int n8;
-  const int* row_info;
+  const int* row_info;  // of row i: its rank in its block, times two, plus one for a BF16 row
   __device__ __forceinline__ void init(const void* pool, int64_t tile_index, int dk, int dv, int n_hp, const int* info) {
     tile = static_cast<const unsigned char*>(pool) + tile_index * q8_tile_bytes(dk, dv, n_hp);
     n8 = dk - n_hp;
     row_info = info;
-  }
-  template <int DV>
-  __device__ __forceinline__ float at(int i, int j) const {
-    constexpr int NG = DV / 32;
-    const int e = row_info[i], idx = e >> 1;
-    if (e & 1)
-      return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(tile + n8 * DV + n8 * NG * 4)[idx * DV + j]);
-    return __fmul_rn((float)reinterpret_cast<const int8_t*>(tile)[idx * DV + j],
-                     reinterpret_cast<const float*>(tile + n8 * DV)[idx * NG + (j >> 5)]);
   }
 };
 
@@ -78,7 +68,7 @@ __device__ __forceinline__ int tree_span(const int32_t* cu, int total, int max_n
 }
 __device__ __forceinline__ uint32_t span_error(int n) { return n == -1 ? LA_DEVERR_CU_SEQLENS : LA_DEVERR_TREE; }
 
-// The same in two steps: the piece as it lies in memory, and its values.
+// Piece c (16 bytes; of INT8 rows 8, with their scale) of row i of a tile as it lies in memory, and its values.
 template <typename ST>
 struct RawPiece {
   uint4 w;
@@ -121,25 +111,14 @@ __device__ __forceinline__ void unpack_piece(const RawPiece<ST>& r, float* x) {
   }
 }
 
-// E consecutive state values, piece c of row i (columns E c ..), in FP32; E = 8, or 4 for FP32 states
-template <int E, typename ST, int DV>
-__device__ __forceinline__ void state_piece(const TileReader<ST>& S, int i, int c, float* x) {
-  if constexpr (std::is_same<ST, q8_t>::value) {
-    constexpr int NG = DV / 32;
-    const int e = S.row_info[i], idx = e >> 1;
-    if (e & 1) {
-      StateVec<__nv_bfloat16>::unpack(
-          __ldcs(reinterpret_cast<const uint4*>(S.tile + S.n8 * DV + S.n8 * NG * 4 + (idx * DV + 8 * c) * 2)), x);
-    } else {
-      const uint2 w = __ldcs(reinterpret_cast<const uint2*>(S.tile + idx * DV + 8 * c));
-      const uint32_t words[2] = {w.x, w.y};
-      q8_unpack<8>(words, reinterpret_cast<const float*>(S.tile + S.n8 * DV)[idx * NG + (c >> 2)], x);
-    }
+// eight consecutive state values (columns 8 c ..) of row i in FP32
+template <typename ST, int DV>
+__device__ __forceinline__ void state_eight(const TileReader<ST>& S, int i, int c, float* x) {
+  if constexpr (std::is_same<ST, float>::value) {
+    unpack_piece(raw_piece<ST, DV>(S, i, 2 * c), x);
+    unpack_piece(raw_piece<ST, DV>(S, i, 2 * c + 1), x + 4);
   } else {
-    constexpr int V = StateVec<ST>::kElems;
-    const uint4* p = reinterpret_cast<const uint4*>(S.tile + i * DV + E * c);
-#pragma unroll
-    for (int e = 0; e < E / V; ++e) StateVec<ST>::unpack(__ldcs(p + e), x + e * V);
+    unpack_piece(raw_piece<ST, DV>(S, i, c), x);
   }
 }
 
@@ -150,12 +129,13 @@ constexpr int kBlock = 16;  // nodes whose products with S0 are formed in one pa
 
 template <int DK, int DV>
 __host__ __device__ constexpr int tree_smem(int rows, bool kda) {
-  return 4 * (rows * DK * (kda ? 3 : 2) + 2 * rows * rows + rows * DV + 2 * kBlock * DV + 3 * rows + DK);
+  return 4 * (rows * DK * (kda ? 3 : 2) + 2 * rows * rows + rows * DV + 2 * kBlock * DV + 3 * rows);
 }
 
-// One CTA per (sequence, state head), FP32 throughout.  The pair coefficients are one warp
-// per node walking to the root; the products with S0 one column of d_v per thread (kBlock
-// nodes per pass); the substitution one column per thread, node after node.
+// The form for heads too narrow for the tensor cores (16 x 16).  One CTA per (sequence, state
+// head), FP32 throughout.  The pair coefficients are one warp per node walking to the root; the
+// products with S0 one column of d_v per thread (kBlock nodes per pass); the substitution one
+// column per thread, node after node.
 template <typename ST, typename IT, int DK, int DV, bool KDA>
 __global__ void __launch_bounds__(kTreeThreads) tree_kernel(const TreeParams p, int rows) {
   extern __shared__ __align__(16) float sm[];
@@ -169,7 +149,6 @@ __global__ void __launch_bounds__(kTreeThreads) tree_kernel(const TreeParams p, 
   float* gamma = buf + 2 * kBlock * DV; // [rows]
   float* gate = gamma + rows;           // [rows] (scalar gates)
   int* par = reinterpret_cast<int*>(gate + rows);  // [rows]
-  int* row_info = par + rows;           // [DK] (q8)
 
   const int H = p.n_v_heads;
   const int b = blockIdx.x / H, h = blockIdx.x % H;
@@ -196,12 +175,6 @@ __global__ void __launch_bounds__(kTreeThreads) tree_kernel(const TreeParams p, 
   }
   if (__syncthreads_or(bad)) {
     if (tid == 0) report(p.err, LA_DEVERR_TREE);
-    return;
-  }
-  bool mask_ok = true;
-  if constexpr (sizeof(ST) == sizeof(q8_t)) mask_ok = q8_rows(p.src_mask + h * (DK / 32), DK, p.src_n_hp, row_info);
-  if (!mask_ok) {
-    if (tid == 0) report(p.err, LA_DEVERR_Q8_MASK);
     return;
   }
   const IT* gq = static_cast<const IT*>(p.q);
@@ -269,7 +242,7 @@ __global__ void __launch_bounds__(kTreeThreads) tree_kernel(const TreeParams p, 
   __syncthreads();
 
   TileReader<ST> S;
-  S.init(p.src, (int64_t)slot * H + h, DK, DV, p.src_n_hp, row_info);
+  S.init(p.src, (int64_t)slot * H + h, DK, DV, 0, nullptr);
   const float* KS = KDA ? KG : K;
   constexpr int NPT = kBlock * DV / kTreeThreads;  // nodes of a thread in one pass
   const int j = tid % DV, grp = tid / DV;

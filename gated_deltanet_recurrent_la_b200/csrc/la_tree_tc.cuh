@@ -465,7 +465,7 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
 #pragma unroll
       for (int e = 0; e < kPieces; ++e) {
         const int at = tid + e * NT;
-        state_piece<8, ST, DV>(S, st * 64 + at / (DV / 8), at % (DV / 8), x[e]);
+        state_eight<ST, DV>(S, st * 64 + at / (DV / 8), at % (DV / 8), x[e]);
       }
       if (st > 0) ok &= tree_wait(bar + 1, (st - 1) & 1);
 #pragma unroll
