@@ -119,6 +119,7 @@ __global__ void __launch_bounds__(kRowThreads, 3) beam_row_kernel(const BeamPara
   __shared__ int winners[LA_BEAM_MAX];
   __shared__ uint64_t tau;
   __shared__ int n_win, n_cand;
+  griddep_wait();
   griddep_launch_dependents();
   const int row = blockIdx.x / parts, part = blockIdx.x % parts, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const float cum = p.cum[row];
@@ -419,9 +420,8 @@ size_t beam_workspace_bytes(int64_t n_seqs, int64_t n_beams, int64_t vocab, int6
 
 cudaError_t launch_beam_select(const BeamParams& p, cudaStream_t stream) {
   const int rows = p.n_seqs * p.n_beams, parts = beam_parts(rows, p.vocab);
-  if (p.io == LA_F32) beam_row_kernel<float><<<rows * parts, kRowThreads, 0, stream>>>(p, parts);
-  else beam_row_kernel<__nv_bfloat16><<<rows * parts, kRowThreads, 0, stream>>>(p, parts);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_dependent(p.io == LA_F32 ? beam_row_kernel<float> : beam_row_kernel<__nv_bfloat16>,
+                                         rows * parts, kRowThreads, 0, stream, p, parts);
   if (e != cudaSuccess) return e;
   const int take = p.n_out < p.vocab ? p.n_out : p.vocab;
   return launch_dependent(beam_merge_kernel, p.n_seqs, kMergeThreads, 8 * p.n_beams * (2 + take), stream, p, parts);

@@ -117,8 +117,8 @@ cudaError_t launch_pool_compact(const SlabList& slabs, int32_t n_slots, const in
 cudaError_t launch_pool_remap(int64_t n, const int32_t* table, int32_t n_slots, const int32_t* remap,
                               int32_t* new_table, int32_t* err, cudaStream_t stream);
 
-// Launch that may start before the stream's previous kernel has drained (the kernel itself
-// waits for it with griddep_wait before it touches memory).
+// Launch that may start before the stream's previous kernel has drained: the kernel itself waits
+// for it (griddep_wait) before it touches memory, so only the launch's own latency overlaps.
 template <typename... P, typename... A>
 cudaError_t launch_dependent(void (*fn)(P...), int grid, int threads, int smem, cudaStream_t stream, const A&... args) {
   cudaLaunchConfig_t cfg{};

@@ -238,6 +238,7 @@ __device__ __forceinline__ int block_rank(bool flag, int* warp_count, int& total
 __global__ void __launch_bounds__(kPlanThreads) alloc_kernel(int32_t* ref, int n_slots, int n, int32_t* slots,
                                                              const int32_t* src, int32_t* err) {
   __shared__ int warp_count[kPlanThreads / 32];
+  griddep_wait();
   int want = n, total;
   uint32_t bad = 0u;
   auto held = [&](int i) {  // before any count changes
@@ -296,6 +297,7 @@ __global__ void __launch_bounds__(kPlanThreads) alloc_kernel(int32_t* ref, int n
 
 __global__ void __launch_bounds__(256) ref_kernel(int32_t* ref, int n_slots, int n, const int32_t* slots, int delta,
                                                   int32_t* err) {
+  griddep_wait();
   const int i = blockIdx.x * 256 + threadIdx.x;
   if (i >= n) return;
   const int s = slots[i];
@@ -318,6 +320,7 @@ __global__ void __launch_bounds__(256) ref_kernel(int32_t* ref, int n_slots, int
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(int n_slots, const int32_t* ref, int32_t* new_ref,
                                                                     int32_t* remap, int32_t* moves, int32_t* counts) {
   __shared__ int warp_count[kPlanThreads / 32];
+  griddep_wait();
   int n_live = 0, total;
   for (int s0 = 0; s0 < n_slots; s0 += kPlanThreads) {
     const int s = s0 + threadIdx.x;
@@ -359,6 +362,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(int n_slots,
 
 __global__ void __launch_bounds__(256) remap_kernel(int64_t n, const int32_t* table, int n_slots, const int32_t* remap,
                                                     int32_t* new_table, int32_t* err) {
+  griddep_wait();
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= n) return;
   const int s = table[i];
@@ -389,20 +393,17 @@ cudaError_t launch_pool_reorder(const SlabList& slabs, int32_t n_slots, int32_t 
 
 cudaError_t launch_pool_alloc(int32_t* ref, int32_t n_slots, int32_t n, int32_t* slots, int32_t* err,
                               cudaStream_t stream) {
-  alloc_kernel<<<1, kPlanThreads, 0, stream>>>(ref, n_slots, n, slots, nullptr, err);
-  return cudaGetLastError();
+  return launch_dependent(alloc_kernel, 1, kPlanThreads, 0, stream, ref, n_slots, n, slots, (const int32_t*)nullptr, err);
 }
 
 cudaError_t launch_pool_ref(int32_t* ref, int32_t n_slots, int32_t n, const int32_t* slots, int32_t delta, int32_t* err,
                             cudaStream_t stream) {
-  ref_kernel<<<(n + 255) / 256, 256, 0, stream>>>(ref, n_slots, n, slots, delta, err);
-  return cudaGetLastError();
+  return launch_dependent(ref_kernel, (n - 1) / 256 + 1, 256, 0, stream, ref, n_slots, n, slots, delta, err);
 }
 
 cudaError_t launch_pool_fork(const SlabList& slabs, int32_t* ref, int32_t n_slots, int32_t n, const int32_t* src_slots,
                              int32_t* new_slots, int32_t* err, cudaStream_t stream) {
-  alloc_kernel<<<1, kPlanThreads, 0, stream>>>(ref, n_slots, n, new_slots, src_slots, err);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_dependent(alloc_kernel, 1, kPlanThreads, 0, stream, ref, n_slots, n, new_slots, src_slots, err);
   if (e != cudaSuccess) return e;
   Pairs q{};
   q.kind = kPairsList;
@@ -416,8 +417,7 @@ cudaError_t launch_pool_fork(const SlabList& slabs, int32_t* ref, int32_t n_slot
 
 cudaError_t launch_pool_compact(const SlabList& slabs, int32_t n_slots, const int32_t* ref, int32_t* new_ref,
                                 int32_t* remap, int32_t* moves, int32_t* counts, int32_t* err, cudaStream_t stream) {
-  compact_plan_kernel<<<1, kPlanThreads, 0, stream>>>(n_slots, ref, new_ref, remap, moves, counts);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_dependent(compact_plan_kernel, 1, kPlanThreads, 0, stream, n_slots, ref, new_ref, remap, moves, counts);
   if (e != cudaSuccess) return e;
   Pairs q{};
   q.kind = kPairsMoves;
@@ -432,8 +432,7 @@ cudaError_t launch_pool_compact(const SlabList& slabs, int32_t n_slots, const in
 
 cudaError_t launch_pool_remap(int64_t n, const int32_t* table, int32_t n_slots, const int32_t* remap,
                               int32_t* new_table, int32_t* err, cudaStream_t stream) {
-  remap_kernel<<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(n, table, n_slots, remap, new_table, err);
-  return cudaGetLastError();
+  return launch_dependent(remap_kernel, (int)((n - 1) / 256 + 1), 256, 0, stream, n, table, n_slots, remap, new_table, err);
 }
 
 }  // namespace la

@@ -24,6 +24,7 @@ namespace {
 // node whose drafted token is the one wanted there; a child lies behind its parent, so the
 // walk ends after at most max_nodes steps.  Bound by latency (a few dependent ballots).
 __global__ void __launch_bounds__(32) accept_kernel(const TreeAcceptParams p) {
+  griddep_wait();
   const int b = blockIdx.x, lane = threadIdx.x;
   const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1);
   if (c0 < 0 || c1 < c0 || c1 > p.total) {
@@ -73,8 +74,7 @@ __global__ void __launch_bounds__(32) accept_kernel(const TreeAcceptParams p) {
 }  // namespace
 
 cudaError_t launch_tree_accept(const TreeAcceptParams& p, cudaStream_t stream) {
-  accept_kernel<<<p.n_seqs, 32, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_dependent(accept_kernel, p.n_seqs, 32, 0, stream, p);
 }
 
 }  // namespace la

@@ -150,6 +150,7 @@ __global__ void __launch_bounds__(kTreeThreads) tree_kernel(const TreeParams p, 
   float* gate = gamma + rows;           // [rows] (scalar gates)
   int* par = reinterpret_cast<int*>(gate + rows);  // [rows]
 
+  griddep_wait();
   const int H = p.n_v_heads;
   const int b = blockIdx.x / H, h = blockIdx.x % H;
   const int hq = h / (H / p.n_qk_heads);
@@ -295,8 +296,7 @@ cudaError_t launch_tree(const TreeParams& p, cudaStream_t stream) {
   auto fn = &tree_kernel<ST, IT, DK, DV, KDA>;
   if (prepare_kernel(reinterpret_cast<const void*>(fn), kTreeThreads, tree_smem<DK, DV>(kMaxNodes, KDA)) <= 0)
     return cudaErrorInvalidConfiguration;
-  fn<<<p.n_seqs * p.n_v_heads, kTreeThreads, tree_smem<DK, DV>(rows, KDA), stream>>>(p, rows);
-  return cudaGetLastError();
+  return launch_dependent(fn, p.n_seqs * p.n_v_heads, kTreeThreads, tree_smem<DK, DV>(rows, KDA), stream, p, rows);
 }
 
 // ---- commit ------------------------------------------------------------------------------------
@@ -344,6 +344,7 @@ __global__ void __launch_bounds__(kCommitThreads, (commit_ctas<ST, DK * DV>())) 
   float* gate = reinterpret_cast<float*>(path + rows);  // [rows]: of the path's nodes
   float* dec = gate + rows;       // [rows]: D_leaf,s (scalar gates)
   int* n_path = reinterpret_cast<int*>(dec + rows);
+  griddep_wait();
   const int H = p.n_v_heads;
   const int b = blockIdx.x / H, h = blockIdx.x % H;
   const int hq = h / (H / p.n_qk_heads);
@@ -508,8 +509,7 @@ cudaError_t launch_commit(const TreeCommitParams& p, cudaStream_t stream) {
   if (prepare_kernel(reinterpret_cast<const void*>(fn), kCommitThreads, commit_smem<DK, DV>(kMaxNodes)) <= 0)
     return cudaErrorInvalidConfiguration;
   const int rows = (p.max_nodes + 3) / 4 * 4;
-  fn<<<p.n_seqs * p.n_v_heads, kCommitThreads, commit_smem<DK, DV>(rows), stream>>>(p, rows);
-  return cudaGetLastError();
+  return launch_dependent(fn, p.n_seqs * p.n_v_heads, kCommitThreads, commit_smem<DK, DV>(rows), stream, p, rows);
 }
 
 }  // namespace tree

@@ -170,6 +170,7 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
   uint64_t* bar = reinterpret_cast<uint64_t*>(row_info + C::kRowInfo);  // A K^T, S0^T A^T
   uint32_t* tm = reinterpret_cast<uint32_t*>(bar + 2);
 
+  griddep_wait();
   const int H = p.n_v_heads;
   const int b = blockIdx.x / H, h = blockIdx.x % H;
   const int hq = h / (H / p.n_qk_heads);
@@ -632,8 +633,7 @@ cudaError_t launch_tree_tc(const TreeParams& p, cudaStream_t stream) {
   static_assert(C::smem(kMaxNodes) <= 227 * 1024, "shared memory");
   if (prepare_kernel(reinterpret_cast<const void*>(fn), C::kThreads, C::smem(kMaxNodes)) <= 0)
     return cudaErrorInvalidConfiguration;
-  fn<<<p.n_seqs * p.n_v_heads, C::kThreads, C::smem(R), stream>>>(p, R);
-  return cudaGetLastError();
+  return launch_dependent(fn, p.n_seqs * p.n_v_heads, C::kThreads, C::smem(R), stream, p, R);
 }
 
 }  // namespace tree
