@@ -52,8 +52,8 @@ struct TcCfg {
   __host__ __device__ static constexpr int term_s(int R) { return DV / 64 * panel_s(R); }
   __host__ __device__ static constexpr int panel_a(int R) { return 2 * R * 128; }
   __host__ __device__ static constexpr int bytes_a(int R) { return TA * PA * panel_a(R); }
-  // operands; over them U [R][DV] and a row of zeros.  A K^T reads 128 rows from any panel of A, S0^T A^T two panels
-  // of 64 columns from any term of S0.
+  // operands; over them U [R][DV] and a row of zeros.  A K^T reads 128 rows from any panel of A,
+  // S0^T A^T two panels of 64 columns from any term of S0.
   __host__ __device__ static constexpr int region(int R) {
     int x = bytes_a(R) + (TS - 1) * term_s(R) + 2 * panel_s(R);
     if (KDA && bytes_a(R) + R * DK * 8 > x) x = bytes_a(R) + R * DK * 8;  // K and g in FP32
@@ -154,7 +154,8 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
     tree_tc_kernel(const TreeParams p, int R) {
   using C = TcCfg<ST, IT, DK, DV, KDA>;
   constexpr int TA = C::TA, TS = C::TS, PA = C::PA, NT = C::kThreads;
-  extern __shared__ __align__(1024) unsigned char tc_smem[];  // (not a rounded pointer: it has to be seen as shared memory)
+  // (not a rounded pointer: the compiler has to see that it is shared memory)
+  extern __shared__ __align__(1024) unsigned char tc_smem[];
   unsigned char* sm = tc_smem;
   const int bytesA = C::bytes_a(R), panelA = C::panel_a(R);
   unsigned char* smA = sm;
@@ -286,7 +287,7 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
   }
   // length and offsets of a record
   auto describe = [&](int t, int m, uint32_t w) {
-    node[t].path = m | path_at(t) << 14 | (m > 4 ? 1 << 31 : 0);
+    node[t].path = m | path_at(t) << 14 | (m > 4 ? INT32_MIN : 0);
     *reinterpret_cast<uint4*>(node[t].at) =
         make_uint4((w & 255u) * (DV * 4), (w >> 8 & 255u) * (DV * 4), (w >> 16 & 255u) * (DV * 4), (w >> 24) * (DV * 4));
   };
