@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kRowThreads, 3) beam_row_kernel(const BeamPara
 #pragma unroll
     for (int e = E - 1; e >= 0; --e)
       if (f[e] == at && pieces.has(pieces.first + where * E + e)) first = pieces.first + where * E + e;
-    if (first >= 0) keys[tid] = beam_key(at, first);
+    if (first >= 0) keys[tid] = beam_key(at + 0.0f, first);  // (-0 as +0)
   }
   // the sums against the largest reference of a warp, then of the CTA
   auto join = [&](float& r, double& x) {
