@@ -3,18 +3,28 @@
 // Candidate (i, v) of a sequence has the score cum_i + x_iv - logsumexp(x_i).  Within a beam
 // the order of the candidates is the order of the logits, so each beam's best n_out come from
 // its logits alone (ties to the lower index), and the sequence's best n_out are among them.
-// Scores are formed and compared in FP64: neighbouring candidates can lie closer than an FP32
-// rounding of a sum of their size, and their order decides whole numbers.
+// Scores are formed of the log-sum and compared in FP64: neighbouring candidates can lie closer
+// than an FP32 rounding of a sum of their size, and their order decides whole numbers.  A
+// log-sum is that of FP32 exponentials, four or eight of them added in FP32 and those sums in
+// FP64: an exponential is off by at most 2^-22 and 2^-22.8 per unit of the distance to its
+// reference, a sum of eight by 2^-21, which leaves about 2^-20 and decides how beams of almost
+// equal scores are ordered.  The sums depend on the row's values alone, not on where it lies, so
+// beams with equal logits and cum_score tie.
 //
 // beam_row_kernel reads a row (or a part of it, where rows are few) once from memory: each
-// thread keeps the place of its best 16-byte piece and a sum of exponentials against a reference
-// that follows the maximum loosely (they stay below e^8, and it seldom moves).  NaN and +inf show
-// in a piece's maximum or sum and send it to a slower form, so nothing is cleaned element by
-// element: about 50 instructions a piece of eight.  The threads form 128 groups; the n_out-th best of the groups' best elements is at
-// or below the row's n_out-th best element, and elements at or above it lie in n_out groups
-// only, so a second look (from L2) at those few per cent of the row finds every candidate:
-// n_out of them and a handful more, which are ranked by counting.  beam_merge_kernel joins the
-// sorted lists.  Bound by the logits' bytes; the exponentials take about as long at BF16.
+// thread keeps the place of its best piece of 16 bytes and a sum of exponentials against a
+// reference that follows the maximum loosely (they stay below e^8, and it seldom moves).  NaN and
+// +inf show in a piece's maximum or sum and send it to a slower form, so nothing is cleaned
+// element by element: about 50 instructions a piece of eight.  The threads form 128 groups; the
+// n_out-th best of the groups' best elements is at or below the row's n_out-th best element, and
+// elements at or above it lie in n_out groups only, so a second look (from L2) at those few per
+// cent of the row finds every candidate: n_out of them and a handful more, which are ranked by
+// counting.  beam_merge_kernel joins the sorted lists.
+// 384 rows of 50257 BF16 logits take 27 us (24 of 50256), of which their bytes are 6 and the
+// exponentials 4: bound by the phases of a single wave of two or three CTAs per SM (reading,
+// groups, ranks, second look), which all pass at the same time.
+#include <type_traits>
+
 #include "la_device.cuh"
 #include "la_serving.h"
 
@@ -56,34 +66,46 @@ __device__ __forceinline__ uint64_t beam_key(float x, int v) {
   return ((uint64_t)beam_order(x) << 32) | (0xffffffffu - (uint32_t)v);
 }
 
-// The 16-byte pieces of elements [lo, hi) of a row, whatever its alignment; the first and the
-// last piece are read element by element.
+// Elements [lo, hi) of a row in pieces of four 4-byte words.  A chunk is 128 words; piece j holds
+// words lane, lane + 32, + 64, + 96 (lane = j % 32) of chunk j / 32, counted from lo wherever the
+// row lies in memory: what a thread adds up, and in which order, depends on the row's values
+// alone, so equal rows have equal sums.  A warp reads a chunk with four coalesced loads.  BF16
+// rows that begin in the middle of a word (`odd`) are turned by a half word between neighbours.
 template <typename IT>
 struct RowPieces {
-  static constexpr int E = 16 / (int)sizeof(IT);
-  const IT* x;
-  int lo, hi, first, n;  // index of piece 0's first element (may lie before lo), number of pieces
-  __device__ __forceinline__ RowPieces(const IT* row, int lo_, int hi_) : x(row), lo(lo_), hi(hi_) {
-    first = lo - (int)((reinterpret_cast<uintptr_t>(row + lo) & 15u) / sizeof(IT));
-    n = hi > lo ? (hi - first + E - 1) / E : 0;
+  static constexpr int W = 4 / (int)sizeof(IT), E = 4 * W, kChunk = 128 * W;  // elements of a word, a piece, a chunk
+  const uint32_t* words;  // the word with element lo
+  int lo, len, odd, chunks;
+  __device__ __forceinline__ RowPieces(const IT* row, int lo_, int hi_) : lo(lo_), len(hi_ - lo_) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(row + lo_);
+    odd = W == 2 ? (int)(at >> 1 & 1u) : 0;
+    words = reinterpret_cast<const uint32_t*>(at & ~(uintptr_t)3);
+    chunks = (len + kChunk - 1) / kChunk;
   }
-  __device__ __forceinline__ bool full(int j) const { return first + j * E >= lo && first + (j + 1) * E <= hi; }
-  __device__ __forceinline__ bool has(int v) const { return v >= lo && v < hi; }
-  __device__ __forceinline__ uint4 load(int j) const {
-    const int v0 = first + j * E;
-    if (full(j)) return __ldg(reinterpret_cast<const uint4*>(x + v0));
-    uint32_t w[4];
-    if constexpr (sizeof(IT) == 4) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) w[e] = has(v0 + e) ? __float_as_uint(x[v0 + e]) : 0xff800000u;
+  // element e of piece j counted from lo (those of a piece rise with e), and whether the row has it
+  static __device__ __forceinline__ int place(int j, int e) { return ((j >> 5) * 128 + (j & 31) + e / W * 32) * W + e % W; }
+  __device__ __forceinline__ bool has(int j, int e) const { return place(j, e) < len; }
+  // whether every word of chunk c, and the one behind it, lies within the elements
+  __device__ __forceinline__ bool inner(int c) const { return c >= odd && (c + 1) * kChunk + odd <= len; }
+  // word i; elements outside are not read and count as -inf
+  __device__ __forceinline__ uint32_t word(int i) const {
+    if constexpr (W == 1) {
+      return i < len ? __ldg(words + i) : 0xff800000u;
     } else {
-      const unsigned short* h = reinterpret_cast<const unsigned short*>(x);
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        w[e] = (has(v0 + 2 * e) ? (uint32_t)h[v0 + 2 * e] : 0xff80u) |
-               (has(v0 + 2 * e + 1) ? (uint32_t)h[v0 + 2 * e + 1] : 0xff80u) << 16;
+      const int a = 2 * i - odd;
+      if (a >= 0 && a + 1 < len) return __ldg(words + i);
+      const unsigned short* h = reinterpret_cast<const unsigned short*>(words + i);
+      return (a >= 0 && a < len ? (uint32_t)h[0] : 0xff80u) | (a + 1 < len ? (uint32_t)h[1] : 0xff80u) << 16;
     }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ __forceinline__ uint4 words_at(int i) const { return make_uint4(word(i), word(i + 32), word(i + 64), word(i + 96)); }
+  static __device__ __forceinline__ uint4 turn(const uint4& w, const uint4& b) {
+    return make_uint4(__funnelshift_r(w.x, b.x, 16), __funnelshift_r(w.y, b.y, 16), __funnelshift_r(w.z, b.z, 16),
+                      __funnelshift_r(w.w, b.w, 16));
+  }
+  __device__ __forceinline__ uint4 load(int j) const {
+    const int i = (j >> 5) * 128 + (j & 31);
+    return odd ? turn(words_at(i), words_at(i + 1)) : words_at(i);
   }
   // of the piece's values f = unpack(w): NaN counts as nothing unless all are
   static __device__ __forceinline__ float largest(const uint4& w, const float* f) {
@@ -145,7 +167,7 @@ __global__ void __launch_bounds__(kRowThreads, 3) beam_row_kernel(const BeamPara
   const RowPieces<IT> pieces(static_cast<const IT*>(p.logits) + (int64_t)row * p.row_stride, lo, hi);
 
   float ref = -INFINITY, at = -INFINITY;
-  int where = -1;  // piece of the thread's first largest element, `at`
+  int where = -1;  // piece with the thread's first largest element, `at`
   double sum = 0.0;
   auto follow = [&](float m, int j) {  // m: the piece's maximum, finite or -inf
     if (m > at || where < 0) {
@@ -180,15 +202,34 @@ __global__ void __launch_bounds__(kRowThreads, 3) beam_row_kernel(const BeamPara
       for (int e = 0; e < E; ++e) s += exponential(f[e]);
     return s;
   };
-  int j = tid;
-  for (; j + 3 * kRowThreads < pieces.n; j += 4 * kRowThreads) {  // four pieces in flight
-    uint4 w[4];
+  constexpr int kWarps = kRowThreads / 32;
+  auto walk = [&](auto odd) {  // a warp reads its chunks
+    auto words = [&](int c, int i) {  // of an inner chunk, from word lane + i
+      const uint32_t* at = pieces.words + c * 128 + lane + i;
+      return make_uint4(__ldg(at), __ldg(at + 32), __ldg(at + 64), __ldg(at + 96));
+    };
+    auto turned = [&](const uint4& w, int c) {  // (the words behind lie in L1 by then)
+      if constexpr (decltype(odd)::value) return pieces.turn(w, words(c, 1));
+      else return w;
+    };
+    for (int c = warp; c < pieces.chunks; c += 4 * kWarps) {
+      if (pieces.inner(c) && pieces.inner(c + 3 * kWarps)) {  // four of them in flight
+        uint4 w[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) w[e] = pieces.load(j + e * kRowThreads);
+        for (int e = 0; e < 4; ++e) w[e] = words(c + e * kWarps, 0);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sum += (double)visit(w[e], j + e * kRowThreads);
-  }
-  for (; j < pieces.n; j += kRowThreads) sum += (double)visit(pieces.load(j), j);
+        for (int e = 0; e < 4; ++e) sum += (double)visit(turned(w[e], c + e * kWarps), (c + e * kWarps) * 32 + lane);
+      } else {
+#pragma unroll 1
+        for (int d = c; d < min(c + 4 * kWarps, pieces.chunks); d += kWarps) {
+          const int j = d * 32 + lane;
+          sum += (double)visit(pieces.inner(d) ? turned(words(d, 0), d) : pieces.load(j), j);
+        }
+      }
+    }
+  };
+  if (pieces.odd) walk(std::true_type{});
+  else walk(std::false_type{});
 
   keys[tid] = 0ull;
   if (where >= 0) {  // the first of the piece's largest elements
@@ -197,7 +238,7 @@ __global__ void __launch_bounds__(kRowThreads, 3) beam_row_kernel(const BeamPara
     int first = -1;
 #pragma unroll
     for (int e = E - 1; e >= 0; --e)
-      if (f[e] == at && pieces.has(pieces.first + where * E + e)) first = pieces.first + where * E + e;
+      if (f[e] == at && pieces.has(where, e)) first = lo + pieces.place(where, e);
     if (first >= 0) keys[tid] = beam_key(at + 0.0f, first);  // (-0 as +0)
   }
   // the sums against the largest reference of a warp, then of the CTA
@@ -254,17 +295,16 @@ __global__ void __launch_bounds__(kRowThreads, 3) beam_row_kernel(const BeamPara
   __syncthreads();
   // (fewer groups than n_out: the part has no more than 64 pieces, and all of it is taken)
   const uint64_t border = tau;
-  const int wins = n_win, per = (pieces.n + kGroups - 1) / kGroups;
+  const int wins = n_win, n_pieces = pieces.chunks * 32, per = (n_pieces + kGroups - 1) / kGroups;
   for (int e = tid; e < wins * per; e += kRowThreads) {
     const int jj = winners[e % wins] + e / wins * kGroups;
-    if (jj >= pieces.n) continue;
+    if (jj >= n_pieces) continue;
     float f[E];
     RowPieces<IT>::values(pieces.load(jj), f);
 #pragma unroll
     for (int c = 0; c < E; ++c) {
-      const int v = pieces.first + jj * E + c;
-      const uint64_t k = beam_key(f[c], v);
-      if (pieces.has(v) && k >= border) {
+      const uint64_t k = beam_key(f[c], lo + pieces.place(jj, c));
+      if (pieces.has(jj, c) && k >= border) {
         const int i = atomicAdd(&n_cand, 1);
         if (i < kCand) keys[i] = k;
       }
@@ -286,14 +326,13 @@ __global__ void __launch_bounds__(kRowThreads, 3) beam_row_kernel(const BeamPara
   uint64_t last = ~0ull;
   for (int r = 0; r < take; ++r) {
     uint64_t k = 0;
-    for (int q = tid; q < pieces.n; q += kRowThreads) {
+    for (int q = tid; q < n_pieces; q += kRowThreads) {
       float f[E];
       RowPieces<IT>::values(pieces.load(q), f);
 #pragma unroll
       for (int c = 0; c < E; ++c) {
-        const int v = pieces.first + q * E + c;
-        const uint64_t x = beam_key(f[c], v);
-        if (pieces.has(v) && x < last && x > k) k = x;
+        const uint64_t x = beam_key(f[c], lo + pieces.place(q, c));
+        if (pieces.has(q, c) && x < last && x > k) k = x;
       }
     }
 #pragma unroll

@@ -547,8 +547,11 @@ la_status la_state_tree_commit(la_rule rule, const la_pool *src, const int32_t *
  *   parent, token   device int32 [n_seqs, n_out];  score: float32;  finished_out: int32 or NULL,
  *               set where the parent was finished or the token is eos_token
  *   workspace   device, 16-byte aligned, at least la_beam_workspace_bytes(...); scratch
- * Logits of -inf are masked tokens, NaN counts as -inf and +inf as the largest float.  Scores are
- * formed and compared in FP64 and rounded once.  n_beams, n_out in 1 .. LA_BEAM_MAX
+ * Logits of -inf are masked tokens, NaN counts as -inf and +inf as the largest float.  A beam's
+ * continuations are ordered by its logits themselves; those of different beams by their scores in
+ * FP64 (rounded once when stored), in which a row's log-sum is good to about 2^-20: beams whose
+ * scores lie closer together may come in either order.  The log-sum depends on the row's values
+ * alone, not on where it lies: beams with equal logits and cum_score tie.  n_beams, n_out in 1 .. LA_BEAM_MAX
  * (LA_ERR_UNSUPPORTED above), n_out <= n_beams * vocab (LA_ERR_SHAPE).  n_seqs == 0 is a no-op. */
 #define LA_BEAM_MAX 64
 size_t la_beam_workspace_bytes(int32_t n_seqs, int32_t n_beams, int32_t vocab, int32_t n_out);

@@ -1,12 +1,15 @@
-"""The order of la_beam_select's continuations where scores are equal: the lower (beam, token)
-first.  Logits are equal as numbers (-0 and +0 are), so the expected orders are exact."""
+"""The order of la_beam_select's continuations where scores are equal.
+
+Equal scores go to the lower (beam, token).  Two logits are equal as numbers (-0 and +0 are), and
+two beams with the same logits and the same cum_score have the same scores wherever their rows
+lie in memory, so the expected orders are exact."""
 import numpy as np
 import pytest
 import torch
 
 import serving_ref as R
 from gated_deltanet_recurrent_la_b200 import lastate as L
-from test_gpu_beam_slots import select
+from test_gpu_beam_slots import beam_inputs, select
 
 pytestmark = pytest.mark.gpu
 F32, BF16 = torch.float32, torch.bfloat16
@@ -48,3 +51,33 @@ def test_zeros_of_either_sign_tie_by_whole_pieces(V, dtype):
     x = sign * torch.where(keep & (sign < 0), 1.0, 0.0)
     assert (x == 0).any() and x.max() == 0
     best(x.to(dtype), torch.tensor([[0.0, -0.25, -0.5]] * 2), 24)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B,K,V", [(3, 4, 5), (2, 8, 97), (2, 4, 4099), (1, 5, 9001), (1, 2, 50257), (40, 8, 5003)])
+def test_equal_beams_tie(B, K, V, dtype):
+    """Rows with the same logits start at every alignment when the vocabulary is odd."""
+    x, _ = beam_inputs(B, 1, V, dtype, seed=V)
+    best(x.expand(B, K, V).contiguous(), torch.full((B, K), -1.375), min(2 * K, V))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_equal_pairs_of_beams_tie(dtype):
+    """Beams 0 and 3, and 1 and 2, have the same logits and cum_score."""
+    x, _ = beam_inputs(4, 2, 10007, dtype, seed=2)
+    best(x[:, [0, 1, 1, 0]].contiguous(), torch.tensor([[-0.5, -0.75, -0.75, -0.5]] * 4), 12)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("V", [1000, 30011])
+def test_scores_do_not_depend_on_where_a_row_lies(V, dtype):
+    """The same rows at every offset: the same bits."""
+    B, K = 1, 3
+    x, cum = beam_inputs(B, K, V, dtype, seed=V + 1)
+    scores = []
+    for offset in range(9):
+        flat = torch.full((offset + B * K * (V + 3) + 16,), 1e9, dtype=dtype, device="cuda")
+        view = flat[offset:offset + B * K * (V + 3)].view(B, K, V + 3)[:, :, :V]
+        view.copy_(x)
+        scores.append(best(x, cum, 7, logits_dev=view))
+    assert all(np.array_equal(s, scores[0]) for s in scores)
