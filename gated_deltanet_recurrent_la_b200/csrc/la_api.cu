@@ -71,6 +71,12 @@ namespace {
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// whether na bytes at a and nb at b (either may be NULL: none) have one in common
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + nb && y < x + na;
+}
+
 int elem_bytes(int32_t dt) { return dt == LA_F32 ? 4 : dt == LA_BF16 ? 2 : 0; }
 
 bool shape_ok(const la_shape& s) {
@@ -782,7 +788,25 @@ la_status la_beam_select(int32_t n_seqs, int32_t n_beams, int32_t vocab, const v
   if (!aligned(logits, elem_bytes(io)) || !aligned(cum_score, 4) || !aligned(finished, 4) || !aligned(parent, 4) ||
       !aligned(token, 4) || !aligned(score, 4) || !aligned(finished_out, 4) || !aligned(workspace, 16))
     return LA_ERR_ALIGN;
-  if (workspace_bytes < la::beam_workspace_bytes(n_seqs, n_beams, vocab, n_out)) return LA_ERR_SHAPE;
+  const size_t need = la::beam_workspace_bytes(n_seqs, n_beams, vocab, n_out);
+  if (workspace_bytes < need) return LA_ERR_SHAPE;
+  // A sequence's inputs are read before its outputs are written, so an output may lie on an
+  // input whose sequences have the same places.
+  const size_t n_in = 4 * (size_t)n_seqs * n_beams, n_res = 4 * (size_t)n_seqs * n_out;
+  const bool in_place = n_out == n_beams || n_seqs == 1;
+  const void* outs[4] = {score, finished_out, parent, token};
+  const void* ins[2] = {cum_score, finished};
+  for (int i = 0; i < 4; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (overlap(outs[i], n_res, outs[j], n_res)) return LA_ERR_ALIAS;
+    for (int j = 0; j < 2; ++j)
+      if (overlap(outs[i], n_res, ins[j], n_in) && !(in_place && i == j && outs[i] == ins[j])) return LA_ERR_ALIAS;
+    if (overlap(outs[i], n_res, workspace, need)) return LA_ERR_ALIAS;
+  }
+  const size_t n_logits = (((size_t)n_seqs * n_beams - 1) * (size_t)row_stride + vocab) * elem_bytes(io);
+  if (overlap(ins[0], n_in, workspace, need) || overlap(ins[1], n_in, workspace, need) ||
+      overlap(logits, n_logits, workspace, need))
+    return LA_ERR_ALIAS;
   la::BeamParams p{};
   p.n_seqs = n_seqs;
   p.n_beams = n_beams;

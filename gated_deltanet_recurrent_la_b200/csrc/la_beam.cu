@@ -375,8 +375,10 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t pb = beam_part_bytes(p.n_out);
   const unsigned char* first = static_cast<const unsigned char*>(p.workspace) + (int64_t)b * K * parts * pb;
+  __shared__ bool done[LA_BEAM_MAX];  // read before anything is written: finished_out may be finished
   griddep_wait();
   if (tid < K) {
+    done[tid] = p.finished && p.finished[(int64_t)b * K + tid] != 0;
     const float cum = p.cum[(int64_t)b * K + tid];
     const unsigned char* w = first + (int64_t)tid * parts * pb;
     float ref = -INFINITY;
@@ -438,7 +440,7 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
       p.parent[to] = i;
       p.token[to] = token;
       p.score[to] = (float)value(i, k);
-      if (p.finished_out) p.finished_out[to] = (p.finished && p.finished[(int64_t)b * K + i] != 0) || token == p.eos;
+      if (p.finished_out) p.finished_out[to] = done[i] || token == p.eos;
       if (w) {
         ++at[1];
         load(1);

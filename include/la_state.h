@@ -547,6 +547,8 @@ la_status la_state_tree_commit(la_rule rule, const la_pool *src, const int32_t *
  *   parent, token   device int32 [n_seqs, n_out];  score: float32;  finished_out: int32 or NULL,
  *               set where the parent was finished or the token is eos_token
  *   workspace   device, 16-byte aligned, at least la_beam_workspace_bytes(...); scratch
+ * With n_out == n_beams, or one sequence, score may be cum_score and finished_out may be finished
+ * (in place).  Otherwise outputs, inputs and workspace do not overlap (LA_ERR_ALIAS).
  * Logits of -inf are masked tokens, NaN counts as -inf and +inf as the largest float.  A beam's
  * continuations are ordered by its logits themselves; those of different beams by their scores in
  * FP64 (rounded once when stored), in which a row's log-sum is good to about 2^-20: beams whose

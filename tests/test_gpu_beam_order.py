@@ -1,4 +1,4 @@
-"""The order of la_beam_select's continuations where scores are equal.
+"""The order of la_beam_select's continuations where scores are equal, and its use in place.
 
 Equal scores go to the lower (beam, token).  Two logits are equal as numbers (-0 and +0 are), and
 two beams with the same logits and the same cum_score have the same scores wherever their rows
@@ -9,7 +9,7 @@ import torch
 
 import serving_ref as R
 from gated_deltanet_recurrent_la_b200 import lastate as L
-from test_gpu_beam_slots import beam_inputs, select
+from test_gpu_beam_slots import beam_inputs, i32, select
 
 pytestmark = pytest.mark.gpu
 F32, BF16 = torch.float32, torch.bfloat16
@@ -81,3 +81,23 @@ def test_scores_do_not_depend_on_where_a_row_lies(V, dtype):
         view.copy_(x)
         scores.append(best(x, cum, 7, logits_dev=view))
     assert all(np.array_equal(s, scores[0]) for s in scores)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("seed", range(3))
+def test_in_place(seed, dtype):
+    """score over cum_score and finished_out over finished, with as many continuations as beams."""
+    B, K, V, eos = 12, 8, 301, 7
+    x, cum = beam_inputs(B, K, V, dtype, seed=seed, masked=0.0)
+    fin = (torch.rand(B, K, generator=torch.Generator().manual_seed(seed)) < 0.4).to(torch.int32)
+    par, tok, sc, fo, gap = R.beam_ref(x, cum.numpy(), fin.numpy(), eos, K)
+    assert gap > 1e-5
+    parent, token, c, f = i32(np.zeros((B, K))), i32(np.zeros((B, K))), cum.cuda(), fin.cuda()
+    ws = torch.empty(L.la_beam_workspace_bytes(B, K, V, K), dtype=torch.uint8, device="cuda")
+    L.check(L.la_beam_select(x.cuda(), c, f, eos, parent, token, c, f, ws))
+    torch.cuda.synchronize()
+    np.testing.assert_array_equal(parent.cpu().numpy(), par)
+    np.testing.assert_array_equal(token.cpu().numpy(), tok)
+    np.testing.assert_array_equal(f.cpu().numpy(), fo)
+    s = c.cpu().numpy()
+    assert np.all(np.abs(s - sc) <= 2.0 ** -20 + 2.0 ** -23 * np.abs(sc))

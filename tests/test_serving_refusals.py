@@ -1,0 +1,41 @@
+"""Refusals of the serving operators that keep their kernels within the caller's arrays (fake,
+never dereferenced device addresses; no call in this file may reach a kernel launch)."""
+import os
+
+import pytest
+
+from gated_deltanet_recurrent_la_b200 import lastate as L
+
+A = 0x7f0000000000
+MB = 1 << 20
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(L.LIB_PATH):
+        from gated_deltanet_recurrent_la_b200 import build
+        build.build()
+    return L.lib()
+
+
+def beam(lib, n=2, K=4, V=100, x=A, io=1, stride=100, cum=A + MB, fin=A + 2 * MB, eos=3, n_out=4, par=A + 3 * MB, tok=A + 4 * MB,
+         sc=A + 5 * MB, fo=A + 6 * MB, ws=A + 7 * MB, nws=MB):
+    return lib.la_beam_select(n, K, V, x, io, stride, cum, fin, eos, n_out, par, tok, sc, fo, ws, nws, None)
+
+
+def test_beam_arrays_that_overlap(lib):
+    """In place only where a sequence's outputs lie on its own inputs."""
+    for n_out in (3, 5):  # of four beams
+        assert beam(lib, n_out=n_out, sc=A + MB) == L.LA_ERR_ALIAS
+        assert beam(lib, n_out=n_out, fo=A + 2 * MB) == L.LA_ERR_ALIAS
+    assert beam(lib, sc=A + MB + 4) == beam(lib, fo=A + 2 * MB - 4) == L.LA_ERR_ALIAS  # shifted by one
+    assert beam(lib, sc=A + 2 * MB) == beam(lib, fo=A + MB) == L.LA_ERR_ALIAS          # the other's input
+    for name in ("par", "tok"):
+        assert beam(lib, **{name: A + MB}) == beam(lib, **{name: A + 2 * MB}) == L.LA_ERR_ALIAS
+    names, at = ("par", "tok", "sc", "fo"), [A + 3 * MB, A + 4 * MB, A + 5 * MB, A + 6 * MB]
+    for i, name in enumerate(names):
+        for j in range(4):
+            if j != i:
+                assert beam(lib, **{name: at[j] + 28}) == L.LA_ERR_ALIAS, (name, j)
+        assert beam(lib, **{name: A + 7 * MB + 8}) == L.LA_ERR_ALIAS                    # the workspace
+    assert beam(lib, ws=A + 64) == beam(lib, ws=A + MB) == beam(lib, ws=A + 2 * MB) == L.LA_ERR_ALIAS
