@@ -90,10 +90,10 @@ struct RowPieces {
   // word i; elements outside are not read and count as -inf
   __device__ __forceinline__ uint32_t word(int i) const {
     if constexpr (W == 1) {
-      return i < len ? __ldg(words + i) : 0xff800000u;
+      return i < len ? ld_coherent(words + i) : 0xff800000u;
     } else {
       const int a = 2 * i - odd;
-      if (a >= 0 && a + 1 < len) return __ldg(words + i);
+      if (a >= 0 && a + 1 < len) return ld_coherent(words + i);
       const unsigned short* h = reinterpret_cast<const unsigned short*>(words + i);
       return (a >= 0 && a < len ? (uint32_t)h[0] : 0xff80u) | (a + 1 < len ? (uint32_t)h[1] : 0xff80u) << 16;
     }
@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kRowThreads, 3) beam_row_kernel(const BeamPara
   auto walk = [&](auto odd) {  // a warp reads its chunks
     auto words = [&](int c, int i) {  // of an inner chunk, from word lane + i
       const uint32_t* at = pieces.words + c * 128 + lane + i;
-      return make_uint4(__ldg(at), __ldg(at + 32), __ldg(at + 64), __ldg(at + 96));
+      return make_uint4(ld_coherent(at), ld_coherent(at + 32), ld_coherent(at + 64), ld_coherent(at + 96));
     };
     auto turned = [&](const uint4& w, int c) {  // (the words behind lie in L1 by then)
       if constexpr (decltype(odd)::value) return pieces.turn(w, words(c, 1));

@@ -133,6 +133,11 @@ __device__ __forceinline__ void cp_async_wait() {
 // Blocks until the preceding kernel on the stream has completed and its memory is
 // visible (a no-op when the launch did not allow programmatic overlap).
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// A load of what the preceding kernel may have written, behind griddep_wait.  A kernel that starts
+// before that one has completed may not take the read-only path (ld.global.nc, __ldg): it asks for
+// data that stays the same for the kernel's whole life, and such a load may move ahead of the wait.
+template <typename T>
+__device__ __forceinline__ T ld_coherent(const T* p) { return *p; }
 // Lets the next kernel on the stream be scheduled (it still waits in griddep_wait).
 __device__ __forceinline__ void griddep_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;"); }
 

@@ -56,7 +56,7 @@ __device__ __forceinline__ int beam_pair(const Pairs& q, int i, int& from, uint3
   uint64_t has = 0, others = 0;  // beams with a child; new beams that are not a first child
   bad = 0u;
   for (int e = 0; e < K; ++e) {
-    const int s = __ldg(slots + e), pe = __ldg(par + e);
+    const int s = ld_coherent(slots + e), pe = ld_coherent(par + e);
     if (s < 0 || s >= q.n_slots) bad |= LA_DEVERR_READ_SLOT;
     if (pe < 0 || pe >= K) {
       bad |= LA_DEVERR_TREE;
@@ -67,12 +67,12 @@ __device__ __forceinline__ int beam_pair(const Pairs& q, int i, int& from, uint3
   }
   from = -1;
   if (bad) return -1;  // this sequence stays as it is
-  const int mine = __ldg(par + j);
-  if (!(others >> j & 1)) return __ldg(slots + mine);
+  const int mine = ld_coherent(par + j);
+  if (!(others >> j & 1)) return ld_coherent(slots + mine);
   uint64_t spare = ~has;
   for (int k = __popcll(others & ((1ull << j) - 1)); k > 0; --k) spare &= spare - 1;
-  from = __ldg(slots + mine);
-  return __ldg(slots + __ffsll((long long)spare) - 1);
+  from = ld_coherent(slots + mine);
+  return ld_coherent(slots + __ffsll((long long)spare) - 1);
 }
 
 __global__ void __launch_bounds__(kCopyWarps * 32) slab_copy_kernel(const SlabList slabs, const Pairs q) {
@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kCopyWarps * 32) slab_copy_kernel(const SlabLi
   }
   __syncwarp();
   griddep_wait();
-  const int n = q.kind == kPairsMoves ? min(q.n, __ldg(q.count)) : q.n;
+  const int n = q.kind == kPairsMoves ? min(q.n, ld_coherent(q.count)) : q.n;
   const int per = slabs.first[slabs.n];
   const int me = warp * (int)gridDim.x + (int)blockIdx.x, step = (int)gridDim.x * kCopyWarps;
   uint32_t loaded = 0, stored = 0;  // lane 0: pieces so far
@@ -126,8 +126,8 @@ __global__ void __launch_bounds__(kCopyWarps * 32) slab_copy_kernel(const SlabLi
           if (bad && i % q.n_beams == 0) report(q.err, bad);
         }
       } else {
-        src = __ldg(q.src + i);
-        if (src >= 0 && src < q.n_slots) dst = __ldg(q.dst + (q.kind == kPairsMoves ? src : i));
+        src = ld_coherent(q.src + i);
+        if (src >= 0 && src < q.n_slots) dst = ld_coherent(q.dst + (q.kind == kPairsMoves ? src : i));
       }
     }
     const bool moves = src >= 0 && src < q.n_slots && dst >= 0 && dst < q.n_slots && dst != src;

@@ -26,7 +26,7 @@ namespace {
 __global__ void __launch_bounds__(32) accept_kernel(const TreeAcceptParams p) {
   griddep_wait();
   const int b = blockIdx.x, lane = threadIdx.x;
-  const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1);
+  const int c0 = ld_coherent(p.cu + b), c1 = ld_coherent(p.cu + b + 1);
   if (c0 < 0 || c1 < c0 || c1 > p.total) {
     if (lane == 0) report(p.err, LA_DEVERR_CU_SEQLENS);
     return;
@@ -44,9 +44,9 @@ __global__ void __launch_bounds__(32) accept_kernel(const TreeAcceptParams p) {
     par[e] = -2;
     tok[e] = tgt[e] = 0;
     if (t < n) {
-      par[e] = __ldg(p.parent + c0 + t);
-      tok[e] = __ldg(p.draft + c0 + t);
-      tgt[e] = __ldg(p.target + c0 + t);
+      par[e] = ld_coherent(p.parent + c0 + t);
+      tok[e] = ld_coherent(p.draft + c0 + t);
+      tgt[e] = ld_coherent(p.target + c0 + t);
       bad |= par[e] < -1 || par[e] >= t;
     }
   }
@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(32) accept_kernel(const TreeAcceptParams p) {
     if (lane == 0) report(p.err, LA_DEVERR_TREE);
     return;
   }
-  int cur = -1, want = __ldg(p.root + b), count = 0;
+  int cur = -1, want = ld_coherent(p.root + b), count = 0;
   for (int step = 0; step < n; ++step) {
     const uint32_t lo = __ballot_sync(0xffffffffu, par[0] == cur && tok[0] == want);
     const uint32_t hi = __ballot_sync(0xffffffffu, par[1] == cur && tok[1] == want);

@@ -46,12 +46,12 @@ struct TileReader<q8_t> {
 // Ranks of a q8 head's rows (threads of the CTA, dk <= blockDim.x); false for a mask that does not hold n_hp rows.
 __device__ __forceinline__ bool q8_rows(const uint32_t* mask, int dk, int n_hp, int* row_info) {
   int count = 0;
-  for (int w = 0; w < dk / 32; ++w) count += __popc(__ldg(mask + w));
+  for (int w = 0; w < dk / 32; ++w) count += __popc(ld_coherent(mask + w));
   if (count != n_hp) return false;
   for (int i = threadIdx.x; i < dk; i += blockDim.x) {
     int below = 0;
-    for (int w = 0; w < i / 32; ++w) below += __popc(__ldg(mask + w));
-    const uint32_t m = __ldg(mask + i / 32);
+    for (int w = 0; w < i / 32; ++w) below += __popc(ld_coherent(mask + w));
+    const uint32_t m = ld_coherent(mask + i / 32);
     below += __popc(m & ((1u << (i & 31)) - 1u));
     const bool hp = (m >> (i & 31)) & 1u;
     row_info[i] = hp ? 2 * below + 1 : 2 * (i - below);
@@ -61,8 +61,8 @@ __device__ __forceinline__ bool q8_rows(const uint32_t* mask, int dk, int n_hp, 
 
 // The nodes of sequence b: c0 and their number, -1 when the offsets or the count are wrong.
 __device__ __forceinline__ int tree_span(const int32_t* cu, int total, int max_nodes, int b, int& c0) {
-  c0 = __ldg(cu + b);
-  const int c1 = __ldg(cu + b + 1);
+  c0 = ld_coherent(cu + b);
+  const int c1 = ld_coherent(cu + b + 1);
   if (c0 < 0 || c1 < c0 || c1 > total) return -1;
   return c1 - c0 > max_nodes ? -2 : c1 - c0;
 }
@@ -162,17 +162,17 @@ __global__ void __launch_bounds__(kTreeThreads) tree_kernel(const TreeParams p, 
     return;
   }
   if (n == 0) return;
-  const int slot = p.read_slot ? __ldg(p.read_slot + b) : b;
+  const int slot = p.read_slot ? ld_coherent(p.read_slot + b) : b;
   if (slot < 0 || slot >= p.src_slots) {
     if (tid == 0) report(p.err, LA_DEVERR_READ_SLOT);
     return;
   }
   bool bad = false;
   for (int t = tid; t < n; t += kTreeThreads) {
-    const int pt = __ldg(p.parent + c0 + t);
+    const int pt = ld_coherent(p.parent + c0 + t);
     bad |= pt < -1 || pt >= t;
     par[t] = pt;
-    if (!KDA) gate[t] = p.g ? __ldg(p.g + (int64_t)(c0 + t) * H + h) : 1.0f;
+    if (!KDA) gate[t] = p.g ? ld_coherent(p.g + (int64_t)(c0 + t) * H + h) : 1.0f;
   }
   if (__syncthreads_or(bad)) {
     if (tid == 0) report(p.err, LA_DEVERR_TREE);
@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kTreeThreads) tree_kernel(const TreeParams p, 
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         if constexpr (KDA) {
-          if (on) d[c] *= __ldg(p.g + ((int64_t)(c0 + s) * H + h) * DK + lane * CH + c);
+          if (on) d[c] *= ld_coherent(p.g + ((int64_t)(c0 + s) * H + h) * DK + lane * CH + c);
         } else {
           d[c] *= gate[s];
         }
@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(kTreeThreads) tree_kernel(const TreeParams p, 
         const int64_t at = ((int64_t)(c0 + t) * H + h) * DV + j;
         float x = io_load(gv + at);
         if (p.predicts) x -= pred;
-        if (p.use_beta) x *= __ldg(p.beta + (int64_t)(c0 + t) * H + h);
+        if (p.use_beta) x *= ld_coherent(p.beta + (int64_t)(c0 + t) * H + h);
         U[t * DV + j] = x;
         if (p.u) p.u[at] = x;
         io_store(static_cast<IT*>(p.o) + at, p.scale * fmaf(QK[t * rows + t], x, out));
@@ -349,10 +349,10 @@ __global__ void __launch_bounds__(kCommitThreads, (commit_ctas<ST, DK * DV>())) 
   const int b = blockIdx.x / H, h = blockIdx.x % H;
   const int hq = h / (H / p.n_qk_heads);
   const int tid = threadIdx.x;
-  const int rs = p.read_slot ? __ldg(p.read_slot + b) : b, ws = p.write_slot ? __ldg(p.write_slot + b) : b;
+  const int rs = p.read_slot ? ld_coherent(p.read_slot + b) : b, ws = p.write_slot ? ld_coherent(p.write_slot + b) : b;
   int c0;
   const int n = tree_span(p.cu, p.total, p.max_nodes, b, c0);
-  const int leaf = __ldg(p.leaf + b);
+  const int leaf = ld_coherent(p.leaf + b);
   if (n < 0) {
     if (tid == 0) report(p.err, span_error(n));
     return;
@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(kCommitThreads, (commit_ctas<ST, DK * DV>())) 
 #pragma unroll
     for (int k = 0; k < NPT; ++k) raw[k] = raw_piece<ST, DV>(S, row0 + k * RS, col);
   }
-  for (int t = tid; t < n; t += kCommitThreads) par[t] = __ldg(p.parent + c0 + t);
+  for (int t = tid; t < n; t += kCommitThreads) par[t] = ld_coherent(p.parent + c0 + t);
   __syncthreads();
   if (tid == 0) {
     int m = 0, s = leaf;
@@ -414,13 +414,13 @@ __global__ void __launch_bounds__(kCommitThreads, (commit_ctas<ST, DK * DV>())) 
       for (int a = 0; a < m; ++a) {
         const int64_t t = c0 + path[a];
         kc[a * DK + i] = d * io_load(gk + (t * p.n_qk_heads + hq) * DK + i);
-        d *= __ldg(p.g + (t * H + h) * DK + i);
+        d *= ld_coherent(p.g + (t * H + h) * DK + i);
       }
       G[i] = d;
     }
   } else if (m > 0) {
     if (p.g) {
-      for (int a = tid; a < m; a += kCommitThreads) gate[a] = __ldg(p.g + (int64_t)(c0 + path[a]) * H + h);
+      for (int a = tid; a < m; a += kCommitThreads) gate[a] = ld_coherent(p.g + (int64_t)(c0 + path[a]) * H + h);
       __syncthreads();
       for (int a = tid; a <= m; a += kCommitThreads) {
         float d = 1.0f;
@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(kCommitThreads, (commit_ctas<ST, DK * DV>())) 
     }
   }
   for (int e = tid; e < m * (DV / 4); e += kCommitThreads)
-    *reinterpret_cast<float4*>(us + 4 * e) = __ldg(reinterpret_cast<const float4*>(
+    *reinterpret_cast<float4*>(us + 4 * e) = ld_coherent(reinterpret_cast<const float4*>(
         p.u + ((int64_t)(c0 + path[e / (DV / 4)]) * H + h) * DV + e % (DV / 4) * 4));
   __syncthreads();
   if (tid >= ACT) return;

@@ -176,7 +176,7 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
   const int b = blockIdx.x / H, h = blockIdx.x % H;
   const int hq = h / (H / p.n_qk_heads);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int slot = p.read_slot ? __ldg(p.read_slot + b) : b;
+  const int slot = p.read_slot ? ld_coherent(p.read_slot + b) : b;
   int c0;
   const int n = tree_span(p.cu, p.total, p.max_nodes, b, c0);
   if (n < 0) {
@@ -195,9 +195,9 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
   int my_par = -1;
   float my_gate = 1.0f, my_beta = 1.0f;
   if (tid < n) {
-    my_par = __ldg(p.parent + c0 + tid);
-    if (!KDA && p.g) my_gate = __ldg(p.g + (int64_t)(c0 + tid) * H + h);
-    if (p.use_beta) my_beta = __ldg(p.beta + (int64_t)(c0 + tid) * H + h);
+    my_par = ld_coherent(p.parent + c0 + tid);
+    if (!KDA && p.g) my_gate = ld_coherent(p.g + (int64_t)(c0 + tid) * H + h);
+    if (p.use_beta) my_beta = ld_coherent(p.beta + (int64_t)(c0 + tid) * H + h);
   }
   // BF16 operands straight to shared memory: the rows of K and Q first, the state behind them
   const IT* gk = static_cast<const IT*>(p.k);
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
   for (int e = 0; e < VN; ++e) {
     const int at = tid + e * NT;
     if (at < n * PV)
-      vr[e] = __ldg(reinterpret_cast<const uint4*>(static_cast<const IT*>(p.v) + base_v + at / PV * step_v) + at % PV);
+      vr[e] = ld_coherent(reinterpret_cast<const uint4*>(static_cast<const IT*>(p.v) + base_v + at / PV * step_v) + at % PV);
   }
 
   // the nodes above; thread t for the coefficients of u, R + t for those of o
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
       const int t = e / (DK / 4), c = e % (DK / 4) * 4;
       load_f32<IT, 4>(gk + row0 + t * row_step + c, Kf + t * DK + c);
       *reinterpret_cast<float4*>(Gf + t * DK + c) =
-          __ldg(reinterpret_cast<const float4*>(p.g + ((int64_t)(c0 + t) * H + h) * DK + c));
+          ld_coherent(reinterpret_cast<const float4*>(p.g + ((int64_t)(c0 + t) * H + h) * DK + c));
     }
     __syncthreads();
     for (int t = warp; t < n; t += NT / 32) {
