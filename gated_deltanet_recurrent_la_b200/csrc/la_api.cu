@@ -20,8 +20,8 @@ namespace la {
 namespace {
 
 thread_local int32_t g_last_cuda_error = 0;
-// failure-path test hooks (la_debug_*): the wait limit of the decode step's pipeline waits,
-// and a one-shot request to withhold one tile's arrival in the next decode step of the thread
+// failure-path test hooks (la_debug_*): the wait limit of the decode step's and the tree
+// verification's waits, and a one-shot request to withhold one tile in the thread's next such call
 thread_local uint64_t g_wait_ns = 0;       // 0: the default limit
 thread_local int64_t g_withhold_tile = -1;
 
@@ -691,6 +691,9 @@ la_status la_state_tree(la_rule rule, const la_pool* src, const int32_t* read_sl
   p.o = o;
   p.u = u;
   p.err = err_word;
+  p.wait_ns = la::g_wait_ns ? la::g_wait_ns : la::kWaitLimitNs;
+  p.withhold = la::g_withhold_tile;
+  la::g_withhold_tile = -1;  // one-shot
   return cuda_status(fn(p, static_cast<cudaStream_t>(stream)));
 }
 

@@ -31,6 +31,10 @@ struct TreeParams {
   void* o;
   float* u;                   // [total, n_v_heads, d_v] or nullptr
   int32_t* err;
+  // failure-path test hooks: the time limit of a wait for products (ns), and a tile (sequence *
+  // n_v_heads + head) whose products with the state are not issued (-1: none)
+  uint64_t wait_ns;
+  int64_t withhold;
 };
 
 struct TreeCommitParams {

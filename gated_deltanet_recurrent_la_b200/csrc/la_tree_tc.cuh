@@ -112,19 +112,30 @@ __device__ __forceinline__ void store_terms(unsigned char* dst, int stride, cons
   }
 }
 
-// Waits for a phase of `bar` at most 2^16 times 20 us, without reading a timer (the thread sleeps
-// in the test itself).  False when it gave up.
-__device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity) {
-  for (uint32_t polls = 0; polls < 1u << 16; ++polls) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_addr(bar)), "r"(parity), "r"(20000u)
-        : "memory");
-    if (done) return true;
+// The thread sleeps in the test itself, up to 20 us.
+__device__ __forceinline__ bool tree_try_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_addr(bar)), "r"(parity), "r"(20000u)
+      : "memory");
+  return done != 0;
+}
+// Waits for a phase of `bar`, without reading a timer where it comes soon.  False when the time
+// limit ran out: then it has waited as long once more, so that the products the phase stands for
+// have ended before their operands and their tensor memory are given up.
+__device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  if (tree_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  bool late = false;
+  for (uint32_t polls = 1; polls < kWaitMaxPolls; ++polls) {
+    if (tree_try_wait(bar, parity)) return !late;
+    const uint64_t t = global_timer_ns() - t0;
+    late = t > limit_ns;
+    if (t > 2 * limit_ns) return false;
   }
   return false;
 }
@@ -406,7 +417,7 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
           }
       umma::commit(bar);
     }
-    ok &= tree_wait(bar, 0);
+    ok = tree_wait(bar, 0, p.wait_ns);
     umma::fence_after();
     if (warp < 4 && warp * 32 < 2 * R) {
       // nearest first: the places fall as s rises
@@ -455,11 +466,13 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
       }
     umma::commit(bar + 1);
   };
+  // (a thread whose wait ran out leaves the operands alone and issues nothing more; all of them learn
+  // of it at the last barrier, and nothing of the tile is written)
   for (int st = 0; st < stages; ++st) {
     if constexpr (TS == 1) {
       if (st > 0) {  // the buffer is free
-        ok &= tree_wait(bar + 1, (st - 1) & 1);
-        state_async(st);
+        if (ok) ok = tree_wait(bar + 1, (st - 1) & 1, p.wait_ns);
+        if (ok) state_async(st);
       }
     } else {
       constexpr int kPieces = 64 * (DV / 8) / NT;
@@ -469,9 +482,10 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
         const int at = tid + e * NT;
         state_eight<ST, DV>(S, st * 64 + at / (DV / 8), at % (DV / 8), x[e]);
       }
-      if (st > 0) ok &= tree_wait(bar + 1, (st - 1) & 1);
+      if (st > 0 && ok) ok = tree_wait(bar + 1, (st - 1) & 1, p.wait_ns);
 #pragma unroll
       for (int e = 0; e < kPieces; ++e) {
+        if (!ok) break;
         const int at = tid + e * NT;
         store_terms<8>(smS + umma::panel_piece(64, at / (DV / 8), at % (DV / 8)), termS, x[e]);
       }
@@ -500,11 +514,11 @@ __global__ void __launch_bounds__((TcCfg<ST, IT, DK, DV, KDA>::kThreads), (TcCfg
     if constexpr (TS == 1) cp_async_wait<0>();
     umma::fence_smem();
     __syncthreads();
-    if (tid == 0) issue(st);
+    if (tid == 0 && ok && (st > 0 || blockIdx.x != p.withhold)) issue(st);
   }
 
   // v in FP32 where U will be
-  ok &= tree_wait(bar + 1, (stages - 1) & 1);
+  if (ok) ok = tree_wait(bar + 1, (stages - 1) & 1, p.wait_ns);
   umma::fence_after();
 #pragma unroll
   for (int e = 0; e < VN; ++e) {
