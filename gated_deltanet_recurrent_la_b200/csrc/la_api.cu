@@ -20,8 +20,8 @@ namespace la {
 namespace {
 
 thread_local int32_t g_last_cuda_error = 0;
-// failure-path test hooks (la_debug_*): the wait limit of the decode step's and the tree
-// verification's waits, and a one-shot request to withhold one tile in the thread's next such call
+// failure-path test hooks (la_debug_*): the wait limit of the decode step, the tree verification
+// and the slot copies, and a one-shot request to withhold one tile in the thread's next such call
 thread_local uint64_t g_wait_ns = 0;       // 0: the default limit
 thread_local int64_t g_withhold_tile = -1;
 
@@ -858,6 +858,14 @@ static la_status slab_list(const la_slab* slabs, int32_t n_slabs, la::SlabList* 
   return LA_OK;
 }
 
+// the failure hooks, for the copies of one call
+static la::SlabList& with_hooks(la::SlabList& list) {
+  list.wait_ns = la::g_wait_ns ? la::g_wait_ns : la::kWaitLimitNs;
+  list.withhold = la::g_withhold_tile;
+  la::g_withhold_tile = -1;  // one-shot
+  return list;
+}
+
 la_status la_state_pool_reorder(const la_slab* slabs, int32_t n_slabs, int32_t n_seqs, int32_t n_beams,
                                 const int32_t* slots, const int32_t* parent, int32_t* new_slots, int32_t* err_word,
                                 void* stream) {
@@ -871,7 +879,7 @@ la_status la_state_pool_reorder(const la_slab* slabs, int32_t n_slabs, int32_t n
   if (!slots || !parent || !new_slots) return LA_ERR_NULL;
   if (!aligned(slots, 4) || !aligned(parent, 4) || !aligned(new_slots, 4) || !aligned(err_word, 4)) return LA_ERR_ALIGN;
   if (new_slots == slots || new_slots == parent) return LA_ERR_ALIAS;
-  return cuda_status(la::launch_pool_reorder(list, slabs[0].n_slots, n_seqs, n_beams, slots, parent, new_slots, err_word,
+  return cuda_status(la::launch_pool_reorder(with_hooks(list), slabs[0].n_slots, n_seqs, n_beams, slots, parent, new_slots, err_word,
                                              static_cast<cudaStream_t>(stream)));
 }
 
@@ -913,7 +921,7 @@ la_status la_state_pool_fork(const la_slab* slabs, int32_t n_slabs, int32_t* ref
   if (!src_slots) return LA_ERR_NULL;
   if (!aligned(src_slots, 4)) return LA_ERR_ALIGN;
   if (src_slots == new_slots || src_slots == ref) return LA_ERR_ALIAS;
-  return cuda_status(la::launch_pool_fork(list, ref, slabs[0].n_slots, n, src_slots, new_slots, err_word,
+  return cuda_status(la::launch_pool_fork(with_hooks(list), ref, slabs[0].n_slots, n, src_slots, new_slots, err_word,
                                           static_cast<cudaStream_t>(stream)));
 }
 
@@ -932,7 +940,7 @@ la_status la_state_pool_compact(const la_slab* slabs, int32_t n_slabs, const int
   for (int i = 0; i < 5; ++i)
     for (int j = 0; j < i; ++j)
       if (all[i] && all[i] == all[j]) return LA_ERR_ALIAS;
-  return cuda_status(la::launch_pool_compact(list, slabs[0].n_slots, ref, new_ref, remap, moves, counts, err_word,
+  return cuda_status(la::launch_pool_compact(with_hooks(list), slabs[0].n_slots, ref, new_ref, remap, moves, counts, err_word,
                                              static_cast<cudaStream_t>(stream)));
 }
 

@@ -106,6 +106,10 @@ struct SlabList {
   void* data[kMaxSlabs];
   int64_t bytes[kMaxSlabs];   // of one slot, a multiple of 16
   int32_t first[kMaxSlabs + 1];  // pieces of a slot before slab l (the launcher's)
+  // failure-path test hooks: the time limit of a wait for a piece (ns), and the piece of the first
+  // warp whose load is not issued (-1: none)
+  uint64_t wait_ns;
+  int64_t withhold;
 };
 cudaError_t launch_pool_reorder(const SlabList& slabs, int32_t n_slots, int32_t n_seqs, int32_t n_beams,
                                 const int32_t* slots, const int32_t* parent, int32_t* new_slots, int32_t* err,

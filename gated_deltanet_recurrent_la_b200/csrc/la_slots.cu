@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kCopyWarps * 32) slab_copy_kernel(const SlabLi
   unsigned char* to_of[kStages];
   auto store = [&] {
     const uint32_t s = stored % kStages;
-    ok = mbar_wait(full + s, (stored / kStages) & 1u);
+    ok = mbar_wait(full + s, (stored / kStages) & 1u, slabs.wait_ns);
     if (!ok) return;
     unsigned char* to = nullptr;
     uint32_t nb = 0;
@@ -180,8 +180,10 @@ __global__ void __launch_bounds__(kCopyWarps * 32) slab_copy_kernel(const SlabLi
               to_of[c] = reinterpret_cast<unsigned char*>(t);
               bytes_of[c] = nb;
             }
-          mbar_arrive_expect_tx(full + s, nb);
-          bulk_g2s(ring + s * kPiece, reinterpret_cast<const void*>(f), nb, full + s);
+          if (me != 0 || loaded != slabs.withhold) {
+            mbar_arrive_expect_tx(full + s, nb);
+            bulk_g2s(ring + s * kPiece, reinterpret_cast<const void*>(f), nb, full + s);
+          }
           ++loaded;
           if (loaded - stored > kLead) store();
         }
@@ -193,7 +195,9 @@ __global__ void __launch_bounds__(kCopyWarps * 32) slab_copy_kernel(const SlabLi
     while (ok && stored < loaded) store();
     if (!ok) {
       report(q.err, LA_DEVERR_TIMEOUT);
-      for (uint32_t e = stored + 1; e < loaded; ++e) mbar_wait(full + e % kStages, (e / kStages) & 1u);
+      // no load may be in flight when the CTA ends: the one that was late gets its limit once more
+      for (uint32_t e = stored; e < loaded; ++e)
+        if (me != 0 || e != slabs.withhold) mbar_wait(full + e % kStages, (e / kStages) & 1u, slabs.wait_ns);
     }
     asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }

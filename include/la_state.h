@@ -641,16 +641,19 @@ int32_t la_abi_version(void);
  * which the kernel stops, reports LA_DEVERR_TIMEOUT through the error word and returns, so
  * the CUDA context stays usable.  These two calls let a test exercise that path without any
  * fault: they change nothing else, and results are unaffected while they are unused.
- *   la_debug_set_wait_limit_us  the limit of the decode step's (la_state_step and its
- *                               variants) and la_state_tree's waits on the calling thread, in
- *                               microseconds; 0 restores the default of one second
+ *   la_debug_set_wait_limit_us  the limit of the waits of the decode step (la_state_step and its
+ *                               variants), of la_state_tree and of the copies of
+ *                               la_state_pool_reorder, _fork and _compact on the calling
+ *                               thread, in microseconds; 0 restores the default of one second
  *   la_debug_withhold_step_tile the next decode step on the calling thread withholds the
  *                               given tile (its index in the first CTA's order, 0 = first):
  *                               the producer issues no copy for it and signals nothing, so
  *                               the consumers' waits run out (nothing is left in flight); one
  *                               call only affects one step; a negative tile cancels it.  If
  *                               la_state_tree comes first, the tile is that of a (sequence,
- *                               head), b H_v + h, whose products with the state are withheld */
+ *                               head), b H_v + h, whose products with the state are withheld;
+ *                               if slot copies come first, a piece of the first warp's, whose
+ *                               load is (the warp's later pieces are not copied either) */
 void la_debug_set_wait_limit_us(uint32_t us);
 void la_debug_withhold_step_tile(int32_t tile);
 

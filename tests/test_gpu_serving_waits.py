@@ -9,6 +9,7 @@ import torch
 
 import serving_ref as R
 from gated_deltanet_recurrent_la_b200 import lastate as L
+from test_gpu_beam_slots import i32, slabs_of
 from test_gpu_tree import device, run_tree
 
 pytestmark = pytest.mark.gpu
@@ -56,3 +57,39 @@ def test_tree_hooks_are_inert_when_not_reached():
     L.la_debug_withhold_step_tile(8)  # tiles 0 .. 7
     again = run_tree(device(inp))
     assert again[2] == 0 and torch.equal(again[0], clean[0]) and torch.equal(again[1], clean[1])
+
+
+def copied(host, dev, src, dst):
+    return all(torch.equal(t[dst], h[src]) for h, t in zip(host, dev))
+
+
+@pytest.mark.parametrize("piece", [0, 1, 4, 9])  # within the first round of the buffers and behind it
+def test_slot_copies_that_do_not_come(piece):
+    """60 slots of 104 pieces of 16 KiB: 12 or more for each of the up to 160 x 3 copying warps."""
+    n_slots, src = 130, list(range(0, 120, 2))
+    host = [t.cuda() for t in slabs_of(n_slots, [1 << 20, 2304, 600000, 16384, 48], 7)]
+    dst = [s + 1 for s in src]
+
+    def fork():
+        dev = [t.clone() for t in host]
+        ref = i32([1 if s in src else 0 for s in range(n_slots)])
+        new, err = i32([55] * len(src)), i32([0])
+        torch.cuda.synchronize()
+        t0 = time.perf_counter()
+        L.check(L.la_state_pool_fork(L.Slabs(dev), ref, i32(src), new, err))
+        torch.cuda.synchronize()
+        assert time.perf_counter() - t0 < 0.5
+        assert new.tolist() == dst
+        return dev, int(err.item())
+
+    dev, err = fork()
+    assert err == 0 and copied(host, dev, src, dst)
+    L.la_debug_set_wait_limit_us(2000)
+    L.la_debug_withhold_step_tile(piece)
+    dev, err = fork()
+    assert err == L.DEVERR_TIMEOUT and not copied(host, dev, src, dst)
+    for h, t in zip(host, dev):  # every byte as it was or that of the slot's source
+        assert torch.equal(t[src], h[src]) and torch.equal(t[120:], h[120:])
+        assert torch.all((t[dst] == h[src]) | (t[dst] == h[dst]))
+    dev, err = fork()  # the hook is one-shot
+    assert err == 0 and copied(host, dev, src, dst)
