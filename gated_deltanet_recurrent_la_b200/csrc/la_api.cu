@@ -767,7 +767,7 @@ la_status la_state_tree_commit(la_rule rule, const la_pool* src, const int32_t* 
 // ---- beam search ----------------------------------------------------------------------------
 
 static la_status check_beam(int32_t n_seqs, int32_t n_beams, int32_t vocab, int32_t n_out) {
-  if (n_seqs < 0 || n_beams < 1 || vocab < 1 || n_out < 1) return LA_ERR_SHAPE;
+  if (n_seqs < 0 || n_beams < 1 || vocab < 1 || vocab > LA_MAX_COUNT || n_out < 1) return LA_ERR_SHAPE;
   if (n_beams > LA_BEAM_MAX || n_out > LA_BEAM_MAX) return LA_ERR_UNSUPPORTED;
   if ((int64_t)n_out > (int64_t)n_beams * vocab || (int64_t)n_seqs * n_beams > INT32_MAX / 64) return LA_ERR_SHAPE;
   return LA_OK;
@@ -845,6 +845,7 @@ static la_status slab_list(const la_slab* slabs, int32_t n_slabs, la::SlabList* 
   if (!slabs) return LA_ERR_NULL;
   if (n_slabs < 1) return LA_ERR_SHAPE;
   if (n_slabs > la::kMaxSlabs) return LA_ERR_UNSUPPORTED;
+  if (slabs[0].n_slots > LA_MAX_COUNT) return LA_ERR_SHAPE;
   out->n = n_slabs;
   for (int32_t l = 0; l < n_slabs; ++l) {
     if (!slabs[l].data) return LA_ERR_NULL;
@@ -885,7 +886,7 @@ la_status la_state_pool_reorder(const la_slab* slabs, int32_t n_slabs, int32_t n
 
 static la_status check_ref(const int32_t* ref, int32_t n_slots, int32_t n, const int32_t* slots, const int32_t* err_word) {
   if (!err_word) return LA_ERR_NULL;
-  if (n_slots < 0 || n < 0) return LA_ERR_SHAPE;
+  if (n_slots < 0 || n_slots > LA_MAX_COUNT || n < 0 || n > LA_MAX_COUNT) return LA_ERR_SHAPE;
   if (n > 0 && (!slots || (n_slots > 0 && !ref))) return LA_ERR_NULL;
   if (!aligned(ref, 4) || !aligned(slots, 4) || !aligned(err_word, 4)) return LA_ERR_ALIGN;
   return n > 0 && slots == ref ? LA_ERR_ALIAS : LA_OK;

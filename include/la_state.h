@@ -553,9 +553,11 @@ la_status la_state_tree_commit(la_rule rule, const la_pool *src, const int32_t *
  * continuations are ordered by its logits themselves; those of different beams by their scores in
  * FP64 (rounded once when stored), in which a row's log-sum is good to about 2^-20: beams whose
  * scores lie closer together may come in either order.  The log-sum depends on the row's values
- * alone, not on where it lies: beams with equal logits and cum_score tie.  n_beams, n_out in 1 .. LA_BEAM_MAX
- * (LA_ERR_UNSUPPORTED above), n_out <= n_beams * vocab (LA_ERR_SHAPE).  n_seqs == 0 is a no-op. */
+ * alone, not on where it lies: beams with equal logits and cum_score tie.  n_beams, n_out in
+ * 1 .. LA_BEAM_MAX (LA_ERR_UNSUPPORTED above), n_out <= n_beams * vocab and vocab <= LA_MAX_COUNT
+ * (LA_ERR_SHAPE).  n_seqs == 0 is a no-op. */
 #define LA_BEAM_MAX 64
+#define LA_MAX_COUNT (2147483647 - 65536) /* of vocabularies and slots: counters are 32 bits */
 size_t la_beam_workspace_bytes(int32_t n_seqs, int32_t n_beams, int32_t vocab, int32_t n_out);
 la_status la_beam_select(int32_t n_seqs, int32_t n_beams, int32_t vocab, const void *logits, la_dtype io,
                          int64_t row_stride, const float *cum_score, const int32_t *finished,
@@ -569,7 +571,8 @@ la_status la_beam_select(int32_t n_seqs, int32_t n_beams, int32_t vocab, const v
  * slab is one of those arrays: n_slots slots of slot_bytes each, contiguous (la_pool_slab makes
  * one of a pool of any dtype; a history is [n_slots] x H_v (2 d_k + d_v) (W - 1) elements).  The
  * slabs of a call (a HOST array, read before the call returns) have one n_slots, slot_bytes a
- * multiple of 16 and 16-byte aligned data, and do not overlap; 1 .. LA_MAX_SLABS of them.
+ * multiple of 16 and 16-byte aligned data, and do not overlap; 1 .. LA_MAX_SLABS of them.  Slots,
+ * and entries of a list of slots, are at most LA_MAX_COUNT (LA_ERR_SHAPE).
  * ("Recurrent state" glossary: slots allocated per active request, compaction, read and write
  * slots of a prefix-cache checkpoint.)  Copies are bit copies.
  *   reorder   beam search: new beam j of sequence b continues old beam parent[b, j].  The first

@@ -39,3 +39,22 @@ def test_beam_arrays_that_overlap(lib):
                 assert beam(lib, **{name: at[j] + 28}) == L.LA_ERR_ALIAS, (name, j)
         assert beam(lib, **{name: A + 7 * MB + 8}) == L.LA_ERR_ALIAS                    # the workspace
     assert beam(lib, ws=A + 64) == beam(lib, ws=A + MB) == beam(lib, ws=A + 2 * MB) == L.LA_ERR_ALIAS
+
+
+TOO_MANY = (1 << 31) - 65536  # one above the largest count
+
+
+def test_counts_that_32_bit_counters_would_pass(lib):
+    """Loops step past the end of a row or a list; near 2^31 their counters would wrap."""
+    big = 1 << 62
+    for n in (TOO_MANY, (1 << 31) - 1):
+        assert beam(lib, V=n, stride=n, ws=big, nws=1 << 40) == L.LA_ERR_SHAPE
+        assert L.la_beam_workspace_bytes(2, 4, n, 4) == 0
+        for fn in (lib.la_state_pool_alloc, lib.la_state_pool_share, lib.la_state_pool_free):
+            assert fn(A, 8, n, A + MB, A, None) == fn(A, n, 8, A + MB, A, None) == L.LA_ERR_SHAPE
+        slabs = (L.la_slab * 1)(L.la_slab(A, 16, 8))
+        assert lib.la_state_pool_fork(slabs, 1, A, n, A + MB, A + 2 * MB, A, None) == L.LA_ERR_SHAPE
+        slabs = (L.la_slab * 1)(L.la_slab(A, 16, n))
+        assert lib.la_state_pool_fork(slabs, 1, A, 3, A + MB, A + 2 * MB, A, None) == L.LA_ERR_SHAPE
+        assert lib.la_state_pool_compact(slabs, 1, A, A + MB, A + 2 * MB, A + 3 * MB, A + 4 * MB, A, None) == L.LA_ERR_SHAPE
+        assert lib.la_state_pool_reorder(slabs, 1, 2, 3, A, A + MB, A + 2 * MB, A, None) == L.LA_ERR_SHAPE
