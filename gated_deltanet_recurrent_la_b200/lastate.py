@@ -187,15 +187,19 @@ def dtype_code(dt: torch.dtype) -> int:
     raise ValueError(f"unsupported dtype {dt}")
 
 
-def _ptr(t: Optional[torch.Tensor], dtype=None):
+def _ptr(t: Optional[torch.Tensor], dtype=None, n: int = 0):
+    """Device pointer of t; n: the least number of entries, where the library takes t's size from
+    another array's."""
     if t is None:
         return None
     if not t.is_cuda:
         raise ValueError("tensor must live on a CUDA device")
     if not t.is_contiguous():
         raise ValueError("tensor must be contiguous")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise ValueError(f"expected {dtype}, got {t.dtype}")
+    if n and t.numel() < n:
+        raise ValueError(f"{n} entries expected, got {t.numel()}")
     return t.data_ptr()
 
 
@@ -527,9 +531,11 @@ def la_state_tree(rule, src: Pool, read_slot, cu_nodes, parent, max_nodes: int, 
     """Outputs o [T, H_v, d_v] (and write vectors u, float32, or None) of the packed drafted
     trees below the pool's states; parent int32 [T], cu_nodes int32 [n_seqs + 1]."""
     io = dtype_code(q.dtype)
+    n = cu_nodes.numel() - 1
+    total = min(q.shape[0], parent.numel())  # cu_nodes beyond it: LA_DEVERR_CU_SEQLENS
     return lib().la_state_tree(RULES[rule] if isinstance(rule, str) else int(rule), src.ref,
-                               _ptr(read_slot, torch.int32), int(cu_nodes.numel() - 1), _ptr(cu_nodes, torch.int32),
-                               int(q.shape[0]), _ptr(parent, torch.int32), int(max_nodes), _ptr(q), _ptr(k, q.dtype),
+                               _ptr(read_slot, torch.int32, n), n, _ptr(cu_nodes, torch.int32),
+                               total, _ptr(parent, torch.int32), int(max_nodes), _ptr(q), _ptr(k, q.dtype),
                                _ptr(v, q.dtype), io, _ptr(g, torch.float32), _ptr(beta, torch.float32), float(scale),
                                _ptr(o, q.dtype), _ptr(u, torch.float32), _ptr(err_word, torch.int32), _stream(stream))
 
@@ -538,21 +544,24 @@ def la_tree_accept(cu_nodes, parent, max_nodes: int, draft, target, root, leaf, 
                    stream=None) -> int:
     """The accepted path of every drafted tree: its last node, its length, the token behind it."""
     i32 = torch.int32
-    return lib().la_tree_accept(int(cu_nodes.numel() - 1), _ptr(cu_nodes, i32), int(parent.numel()), _ptr(parent, i32),
-                                int(max_nodes), _ptr(draft, i32), _ptr(target, i32), _ptr(root, i32), _ptr(leaf, i32),
-                                _ptr(count, i32), _ptr(next_token, i32), _ptr(err_word, i32), _stream(stream))
+    n = cu_nodes.numel() - 1
+    total = min(parent.numel(), draft.numel(), target.numel())  # cu_nodes beyond it: LA_DEVERR_CU_SEQLENS
+    return lib().la_tree_accept(n, _ptr(cu_nodes, i32), total, _ptr(parent, i32), int(max_nodes), _ptr(draft, i32),
+                                _ptr(target, i32), _ptr(root, i32, n), _ptr(leaf, i32, n), _ptr(count, i32, n),
+                                _ptr(next_token, i32, n), _ptr(err_word, i32), _stream(stream))
 
 
 def la_state_tree_commit(rule, src: Pool, read_slot, dst: Pool, write_slot, cu_nodes, parent, leaf, max_nodes: int, k, g, u,
                          err_word, stream=None) -> int:
     """The state after each sequence's node leaf[b], from the write vectors la_state_tree kept."""
     io = dtype_code(k.dtype)
+    n = cu_nodes.numel() - 1
+    total = min(k.shape[0], parent.numel())  # cu_nodes beyond it: LA_DEVERR_CU_SEQLENS
     return lib().la_state_tree_commit(RULES[rule] if isinstance(rule, str) else int(rule), src.ref,
-                                      _ptr(read_slot, torch.int32), dst.ref, _ptr(write_slot, torch.int32),
-                                      int(cu_nodes.numel() - 1), _ptr(cu_nodes, torch.int32), int(k.shape[0]),
-                                      _ptr(parent, torch.int32), _ptr(leaf, torch.int32), int(max_nodes), _ptr(k), io,
-                                      _ptr(g, torch.float32), _ptr(u, torch.float32), _ptr(err_word, torch.int32),
-                                      _stream(stream))
+                                      _ptr(read_slot, torch.int32, n), dst.ref, _ptr(write_slot, torch.int32, n), n,
+                                      _ptr(cu_nodes, torch.int32), total, _ptr(parent, torch.int32),
+                                      _ptr(leaf, torch.int32, n), int(max_nodes), _ptr(k), io, _ptr(g, torch.float32),
+                                      _ptr(u, torch.float32), _ptr(err_word, torch.int32), _stream(stream))
 
 
 # ---- beam search ----------------------------------------------------------------------------
@@ -568,16 +577,18 @@ def la_beam_select(logits, cum_score, finished, eos_token: int, parent, token, s
     (rows may be further apart than vocab, as those of a slice), cum_score float32 [n_seqs,
     n_beams], finished int32 or None; workspace: la_beam_workspace_bytes(...) uint8."""
     B, K, V = logits.shape
-    stride = logits.stride(1) if K > 1 else logits.stride(0) if B > 1 else V
+    s0, s1, s2 = logits.stride()
+    stride = s1 if K > 1 else s0 if B > 1 else V
     if not logits.is_cuda:
         raise ValueError("tensor must live on a CUDA device")
-    if (V > 1 and logits.stride(2) != 1) or (B > 1 and K > 1 and logits.stride(0) != K * stride):
+    if (V > 1 and s2 != 1) or (B > 1 and K > 1 and s0 != K * stride):
         raise ValueError("logits must be rows of contiguous values, equally far apart")
-    i32 = torch.int32
-    return lib().la_beam_select(B, K, V, ctypes.c_void_p(logits.data_ptr()), dtype_code(logits.dtype), int(stride),
-                                _ptr(cum_score, torch.float32), _ptr(finished, i32), int(eos_token),
-                                int(parent.shape[1]), _ptr(parent, i32), _ptr(token, i32), _ptr(score, torch.float32),
-                                _ptr(finished_out, i32), _ptr(workspace), int(workspace.numel() * workspace.element_size()),
+    i32, f32 = torch.int32, torch.float32
+    n_in, n_out = B * K, parent.shape[1]
+    n = B * n_out
+    return lib().la_beam_select(B, K, V, logits.data_ptr(), dtype_code(logits.dtype), stride, _ptr(cum_score, f32, n_in),
+                                _ptr(finished, i32, n_in), int(eos_token), n_out, _ptr(parent, i32, n), _ptr(token, i32, n),
+                                _ptr(score, f32, n), _ptr(finished_out, i32, n), _ptr(workspace), workspace.nbytes,
                                 _stream(stream))
 
 
@@ -607,8 +618,9 @@ class Slabs:
 def la_state_pool_reorder(slabs: Slabs, slots, parent, new_slots, err_word, stream=None) -> int:
     """slots, parent, new_slots int32 [n_seqs, n_beams]: new beam j continues old beam parent[b, j]."""
     i32 = torch.int32
-    return lib().la_state_pool_reorder(slabs.array, slabs.n, int(slots.shape[0]), int(slots.shape[1]), _ptr(slots, i32),
-                                       _ptr(parent, i32), _ptr(new_slots, i32), _ptr(err_word, i32), _stream(stream))
+    B, K = slots.shape[0], slots.shape[1]
+    return lib().la_state_pool_reorder(slabs.array, slabs.n, B, K, _ptr(slots, i32), _ptr(parent, i32, B * K),
+                                       _ptr(new_slots, i32, B * K), _ptr(err_word, i32), _stream(stream))
 
 
 def la_state_pool_alloc(ref, slots, err_word, stream=None) -> int:
@@ -653,5 +665,6 @@ def la_state_pool_compact(slabs: Slabs, ref, new_ref, remap, moves, counts, err_
 def la_state_pool_remap(table, remap, new_table, err_word, stream=None) -> int:
     """new_table[i] <- remap[table[i]]; -1 stays."""
     i32 = torch.int32
-    return lib().la_state_pool_remap(int(table.numel()), _ptr(table, i32), int(remap.numel()), _ptr(remap, i32),
-                                     _ptr(new_table, i32), _ptr(err_word, i32), _stream(stream))
+    n = table.numel()
+    return lib().la_state_pool_remap(n, _ptr(table, i32), remap.numel(), _ptr(remap, i32), _ptr(new_table, i32, n),
+                                     _ptr(err_word, i32), _stream(stream))
