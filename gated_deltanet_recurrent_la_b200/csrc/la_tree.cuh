@@ -398,7 +398,10 @@ __global__ void __launch_bounds__(kCommitThreads, (commit_ctas<ST, DK * DV>())) 
     return;
   }
   if constexpr (Q8) {
-    if (m == 0 && p.src_mask == p.dst_mask) {  // nothing accepted: the tile as it is
+    bool same = m == 0;  // nothing accepted, and the rows of one kind in both pools: the tile as it is
+    for (int w = 0; same && w < DK / 32; ++w)
+      same = ld_coherent(p.src_mask + h * (DK / 32) + w) == ld_coherent(p.dst_mask + h * (DK / 32) + w);
+    if (same) {
       const int64_t bytes = q8_tile_bytes(DK, DV, p.n_hp);
       const uint4* s = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(p.src) + ((int64_t)rs * H + h) * bytes);
       uint4* d = reinterpret_cast<uint4*>(static_cast<unsigned char*>(p.dst) + ((int64_t)ws * H + h) * bytes);

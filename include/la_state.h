@@ -524,7 +524,7 @@ la_status la_tree_accept(int32_t n_seqs, const int32_t *cu_nodes, int32_t total_
  *   S <- Gamma_leaf S + sum over the path's nodes s of (D_leaf,s k_s) u_s^T
  * (Gamma, D: products of the gates along the path), read at src slot read_slot[b] (NULL: slot b)
  * and written at dst slot write_slot[b] (NULL: slot b), rounded once.  leaf[b] == -1: the state is
- * copied.  A sequence may read and write one slot.  src and dst have one shape and dtype (q8:
+ * copied as it is (between q8 masks that differ, re-encoded).  A sequence may read and write one slot.  src and dst have one shape and dtype (q8:
  * equal n_hp; LA_ERR_ALIAS for one pool with two mask arrays).  linear and gated rules take u
  * from la_state_tree too (there u = v).  g as la_state_tree (ignored by linear and delta). */
 la_status la_state_tree_commit(la_rule rule, const la_pool *src, const int32_t *read_slot,
