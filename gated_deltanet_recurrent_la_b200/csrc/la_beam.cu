@@ -45,8 +45,9 @@ struct BeamPart {   // of one part of a row: then n_out keys (order of the logit
 };
 __host__ __device__ constexpr int64_t beam_part_bytes(int n_out) { return (int64_t)sizeof(BeamPart) + 8 * (int64_t)n_out; }
 
-// Parts of a row: enough of them for two CTAs per SM, of 4096 elements at least (below that the
-// merge costs more than the reading).
+// Parts of a row: enough of them for two CTAs on each of a B200's 148 SMs, of 4096 elements at
+// least (below that the merge costs more than the reading).  A number of the sizes alone, so that
+// a row's sums are the same on every device and in every workspace.
 int beam_parts(int64_t rows, int64_t vocab) {
   int64_t s = (2 * 148 + rows - 1) / rows;
   if (s > vocab / 4096) s = vocab / 4096;

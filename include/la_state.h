@@ -110,7 +110,8 @@ typedef enum {
 #define LA_DEVERR_READ_SLOT 1u  /* a read / source slot index outside [0, n_slots) */
 #define LA_DEVERR_WRITE_SLOT 2u /* a write / destination slot index outside [0, n_slots) */
 #define LA_DEVERR_CU_SEQLENS 4u /* cu_seqlens not non-decreasing within [0, total_tokens], or a bad seq_order entry */
-#define LA_DEVERR_TIMEOUT 8u    /* an internal pipeline wait gave up (should never happen) */
+#define LA_DEVERR_TIMEOUT 8u    /* an internal pipeline wait gave up, or a kernel's shared memory was not
+                                   aligned as it asked (should never happen) */
 #define LA_DEVERR_Q8_MASK 16u   /* a q8 head's channel mask does not hold exactly n_hp rows */
 #define LA_DEVERR_TREE 32u      /* a tree with a parent not before its child, more nodes than max_nodes or a
                                    leaf outside it; a beam's parent outside [0, n_beams) */
@@ -493,6 +494,9 @@ la_status la_state_pool_decode(const la_pool *pool, int32_t n, const int32_t *sl
  *   q, k            [total_nodes, H_qk, d_k];  v, o: [total_nodes, H_v, d_v] (io dtype);
  *   g, beta         as la_state_scan
  *   u               device float32 [total_nodes, H_v, d_v], 16-byte aligned, or NULL
+ * q, k, v are those that enter the recurrence: for a layer with the short convolution ahead of it
+ * (la_state_step_conv) the caller convolves along each node's path, and takes the convolution
+ * history along the accepted path; la_state_tree_commit moves the state alone.
  * A sequence without nodes is left alone.  Gates of zero and of either sign are exact (decays
  * are products along the path, never ratios), and a non-finite value reaches only the nodes
  * below it.  FP32 arithmetic; the products with the state and among the nodes run on the tensor
@@ -524,9 +528,11 @@ la_status la_tree_accept(int32_t n_seqs, const int32_t *cu_nodes, int32_t total_
  *   S <- Gamma_leaf S + sum over the path's nodes s of (D_leaf,s k_s) u_s^T
  * (Gamma, D: products of the gates along the path), read at src slot read_slot[b] (NULL: slot b)
  * and written at dst slot write_slot[b] (NULL: slot b), rounded once.  leaf[b] == -1: the state is
- * copied as it is (between q8 masks that differ, re-encoded).  A sequence may read and write one slot.  src and dst have one shape and dtype (q8:
- * equal n_hp; LA_ERR_ALIAS for one pool with two mask arrays).  linear and gated rules take u
- * from la_state_tree too (there u = v).  g as la_state_tree (ignored by linear and delta). */
+ * copied as it is (between q8 masks that differ, re-encoded).  A sequence may read and write one
+ * slot; write slots are distinct and none is another sequence's read slot in the same array.  src
+ * and dst have one shape and dtype (q8: equal n_hp; LA_ERR_ALIAS for one pool with two mask
+ * arrays).  linear and gated rules take u from la_state_tree too (there u = v).  g as
+ * la_state_tree (ignored by linear and delta). */
 la_status la_state_tree_commit(la_rule rule, const la_pool *src, const int32_t *read_slot,
                                const la_pool *dst, const int32_t *write_slot, int32_t n_seqs,
                                const int32_t *cu_nodes, int32_t total_nodes, const int32_t *parent,
