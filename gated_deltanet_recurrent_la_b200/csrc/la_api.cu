@@ -74,7 +74,7 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 // whether na bytes at a and nb at b (either may be NULL: none) have one in common
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a && b && x < y + nb && y < x + na;
+  return a && b && na && nb && x < y + nb && y < x + na;
 }
 
 int elem_bytes(int32_t dt) { return dt == LA_F32 ? 4 : dt == LA_BF16 ? 2 : 0; }
@@ -879,7 +879,8 @@ la_status la_state_pool_reorder(const la_slab* slabs, int32_t n_slabs, int32_t n
   if (n_seqs == 0) return LA_OK;
   if (!slots || !parent || !new_slots) return LA_ERR_NULL;
   if (!aligned(slots, 4) || !aligned(parent, 4) || !aligned(new_slots, 4) || !aligned(err_word, 4)) return LA_ERR_ALIGN;
-  if (new_slots == slots || new_slots == parent) return LA_ERR_ALIAS;
+  const size_t bytes = 4 * (size_t)n_seqs * n_beams;
+  if (overlap(new_slots, bytes, slots, bytes) || overlap(new_slots, bytes, parent, bytes)) return LA_ERR_ALIAS;
   return cuda_status(la::launch_pool_reorder(with_hooks(list), slabs[0].n_slots, n_seqs, n_beams, slots, parent, new_slots, err_word,
                                              static_cast<cudaStream_t>(stream)));
 }
@@ -889,7 +890,7 @@ static la_status check_ref(const int32_t* ref, int32_t n_slots, int32_t n, const
   if (n_slots < 0 || n_slots > LA_MAX_COUNT || n < 0 || n > LA_MAX_COUNT) return LA_ERR_SHAPE;
   if (n > 0 && (!slots || (n_slots > 0 && !ref))) return LA_ERR_NULL;
   if (!aligned(ref, 4) || !aligned(slots, 4) || !aligned(err_word, 4)) return LA_ERR_ALIGN;
-  return n > 0 && slots == ref ? LA_ERR_ALIAS : LA_OK;
+  return overlap(slots, 4 * (size_t)n, ref, 4 * (size_t)n_slots) ? LA_ERR_ALIAS : LA_OK;
 }
 
 la_status la_state_pool_alloc(int32_t* ref, int32_t n_slots, int32_t n, int32_t* slots, int32_t* err_word, void* stream) {
@@ -921,7 +922,9 @@ la_status la_state_pool_fork(const la_slab* slabs, int32_t n_slabs, int32_t* ref
   if ((st = check_ref(ref, slabs[0].n_slots, n, new_slots, err_word)) != LA_OK || n == 0) return st;
   if (!src_slots) return LA_ERR_NULL;
   if (!aligned(src_slots, 4)) return LA_ERR_ALIGN;
-  if (src_slots == new_slots || src_slots == ref) return LA_ERR_ALIAS;
+  const size_t bytes = 4 * (size_t)n;
+  if (overlap(src_slots, bytes, new_slots, bytes) || overlap(src_slots, bytes, ref, 4 * (size_t)slabs[0].n_slots))
+    return LA_ERR_ALIAS;
   return cuda_status(la::launch_pool_fork(with_hooks(list), ref, slabs[0].n_slots, n, src_slots, new_slots, err_word,
                                           static_cast<cudaStream_t>(stream)));
 }
@@ -938,9 +941,10 @@ la_status la_state_pool_compact(const la_slab* slabs, int32_t n_slabs, const int
       !aligned(err_word, 4))
     return LA_ERR_ALIGN;
   const int32_t* all[5] = {ref, new_ref, remap, moves, counts};
+  const size_t bytes = 4 * (size_t)slabs[0].n_slots;
   for (int i = 0; i < 5; ++i)
     for (int j = 0; j < i; ++j)
-      if (all[i] && all[i] == all[j]) return LA_ERR_ALIAS;
+      if (overlap(all[i], i == 4 ? 8 : bytes, all[j], bytes)) return LA_ERR_ALIAS;
   return cuda_status(la::launch_pool_compact(with_hooks(list), slabs[0].n_slots, ref, new_ref, remap, moves, counts, err_word,
                                              static_cast<cudaStream_t>(stream)));
 }
@@ -952,7 +956,9 @@ la_status la_state_pool_remap(int64_t n, const int32_t* table, int32_t n_slots, 
   if (n == 0) return LA_OK;
   if (!table || !new_table || (n_slots > 0 && !remap)) return LA_ERR_NULL;
   if (!aligned(table, 4) || !aligned(remap, 4) || !aligned(new_table, 4) || !aligned(err_word, 4)) return LA_ERR_ALIGN;
-  if (new_table == remap) return LA_ERR_ALIAS;
+  const size_t bytes = 4 * (size_t)n;
+  if (overlap(new_table, bytes, remap, 4 * (size_t)n_slots) || (new_table != table && overlap(new_table, bytes, table, bytes)))
+    return LA_ERR_ALIAS;
   return cuda_status(la::launch_pool_remap(n, table, n_slots, remap, new_table, err_word,
                                            static_cast<cudaStream_t>(stream)));
 }

@@ -605,7 +605,9 @@ la_status la_beam_select(int32_t n_seqs, int32_t n_beams, int32_t vocab, const v
  *             Five different arrays (LA_ERR_ALIAS)
  *   remap     new_table[i] <- remap[table[i]] (table may be new_table); -1 stays, a slot outside
  *             [0, n_slots) stays and reports LA_DEVERR_READ_SLOT
- * Calls on the same arrays are ordered by the caller (one stream). */
+ * Arrays that are called different do not overlap either, nor do ref and a list of slots, nor a
+ * shifted table and new_table (LA_ERR_ALIAS).  Calls on the same arrays are ordered by the caller
+ * (one stream). */
 #define LA_MAX_SLABS 128
 typedef struct {
     void *data;         /* device, 16-byte aligned */

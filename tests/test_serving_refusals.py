@@ -58,3 +58,30 @@ def test_counts_that_32_bit_counters_would_pass(lib):
         assert lib.la_state_pool_fork(slabs, 1, A, 3, A + MB, A + 2 * MB, A, None) == L.LA_ERR_SHAPE
         assert lib.la_state_pool_compact(slabs, 1, A, A + MB, A + 2 * MB, A + 3 * MB, A + 4 * MB, A, None) == L.LA_ERR_SHAPE
         assert lib.la_state_pool_reorder(slabs, 1, 2, 3, A, A + MB, A + 2 * MB, A, None) == L.LA_ERR_SHAPE
+
+
+def test_lists_of_slots_that_overlap(lib):
+    """By a few entries, where both arrays are written or read by many threads at once."""
+    slabs = (L.la_slab * 1)(L.la_slab(A, 16, 8))
+    B = A + MB
+    for d in (-20, -4, 4, 20):  # 6 beams: 24 bytes
+        assert lib.la_state_pool_reorder(slabs, 1, 2, 3, B, B + 512, B + d, A, None) == L.LA_ERR_ALIAS
+        assert lib.la_state_pool_reorder(slabs, 1, 2, 3, B + 512, B, B + d, A, None) == L.LA_ERR_ALIAS
+    for fn in (lib.la_state_pool_alloc, lib.la_state_pool_share, lib.la_state_pool_free):  # 8 counts, 3 slots
+        assert [fn(B, 8, 3, B + d, A, None) for d in (-8, 4, 28)] == [L.LA_ERR_ALIAS] * 3
+    assert lib.la_state_pool_fork(slabs, 1, B, 3, B + 64, B + 72, A, None) == L.LA_ERR_ALIAS
+    assert lib.la_state_pool_fork(slabs, 1, B, 3, B + 28, B + 72, A, None) == L.LA_ERR_ALIAS
+    assert lib.la_state_pool_fork(slabs, 1, B, 3, B + 72, B + 28, A, None) == L.LA_ERR_ALIAS
+    good = [B, B + 64, B + 128, B + 192, B + 256]  # 8 slots: 32 bytes, and the counts
+    for i in range(5):
+        for j in range(5):
+            if j != i:
+                ptrs = [good[j] + 4 if k == i else p for k, p in enumerate(good)]
+                assert lib.la_state_pool_compact(slabs, 1, *ptrs, A, None) == L.LA_ERR_ALIAS, (i, j)
+    assert lib.la_state_pool_remap(5, B, 8, B + 64, B + 4, A, None) == L.LA_ERR_ALIAS
+    assert lib.la_state_pool_remap(5, B, 8, B + 64, B + 48, A, None) == L.LA_ERR_ALIAS
+
+
+def test_empty_lists_overlap_nothing(lib):
+    for fn in (lib.la_state_pool_alloc, lib.la_state_pool_share, lib.la_state_pool_free):
+        assert fn(A, 8, 0, A + 8, A, None) == L.LA_OK
